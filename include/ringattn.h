@@ -258,6 +258,82 @@ int ring_attn_decode(const void* q, const void* k, const void* v, void* out, flo
                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * A serving cache: rows of K and V for B sequences, each with its own length, kept in a
+ * format of fewer bits. All tensors row-major and contiguous:
+ *   k_cache, v_cache  [B, Hkv, capacity, D] bf16, or [.., D] e4m3 bytes, or [.., D/2]
+ *                     bytes of two e2m1 codes (element 2i in the low half of byte i)
+ *   k_scale, v_scale  [B, Hkv, capacity, D/32] bytes (microscaled formats; NULL for bf16)
+ * Microscaled formats: along the head dimension, 32 values share one power of two 2^k,
+ * stored as the byte k + 127, k being the smallest integer (>= -127) with
+ * max|x| <= M 2^k; the elements are x 2^-k rounded to nearest even. M = 448 for MXFP8
+ * (e4m3), 6 for MXFP4 (e2m1). Byte 255 marks a block that holds a NaN or an infinity; it
+ * reads as NaN. capacity % 16 == 0, capacity <= 2^30, D in {64, 128}.
+ */
+#define RING_ATTN_CACHE_BF16 0
+#define RING_ATTN_CACHE_MXFP8 1
+#define RING_ATTN_CACHE_MXFP4 2
+
+/*
+ * Writes T rows per sequence and kv head: cache row start[b] + i becomes new row i, or new
+ * row index[b, i] where index is given (the accepted nodes of a drafted tree, say).
+ *   k_new, v_new  device [B, Hkv, T_src, D] in dtype, element strides of (b, h, t) in
+ *                 strides[0..2] (k) and strides[3..5] (v), a host array; the head
+ *                 dimension is contiguous and every stride a multiple of 16 bytes
+ *   start [B], count [B] or NULL (all T rows), index [B, T] or NULL: device int32
+ *   workspace     device scratch of >= 256 bytes for the status word, or NULL
+ * Row i is written only where i < count[b]. A row that would fall outside the cache, and
+ * an index outside [0, T_src), is skipped and reported as RING_ATTN_EINVAL by
+ * ring_attn_status (when a workspace was given), as is a count above T. No other row of
+ * the cache is touched. The new rows must not overlap the cache; two rows of one call
+ * always fall on different cache rows.
+ */
+int ring_attn_cache_write(const void* k_new, const void* v_new, const int64_t* strides, int dtype,
+                          void* k_cache, void* v_cache, void* k_scale, void* v_scale, int format,
+                          int B, int Hkv, int64_t capacity, int D, int T, int T_src,
+                          const int32_t* start, const int32_t* count, const int32_t* index,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Reads rows back as the values they stand for: k_out, v_out [B, Hkv, T, D] in dtype
+ * (contiguous), row i from cache row start[b] + i. Rows i >= count[b] (count may be NULL)
+ * and rows outside the cache are zeros. In bf16 every microscaled value is exact (down to
+ * bf16's subnormals, where it is rounded to nearest even).
+ */
+int ring_attn_cache_read(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                         int format, int B, int Hkv, int64_t capacity, int D, int T,
+                         const int32_t* start, const int32_t* count, void* k_out, void* v_out, int dtype,
+                         void* stream);
+
+/*
+ * Attention of drafted tokens over a cache, for verifying a tree of them in one call, a
+ * chain, or one token (ordinary decoding, T = 1). Sequence b has lengths[b] committed rows
+ * in its cache; its drafted node j, already written, is cache row lengths[b] + j. With
+ * parents [B, T] (node j's parent in [-1, j); -1: a child of the last committed token) node
+ * t sees every committed token, its ancestors and itself; parents = NULL is a chain.
+ * counts [B] (or NULL: T) gives the live nodes; rows of dead nodes get out = 0 and
+ * lse = -inf.
+ *   window  0, or the number of latest positions a node sees, its own included: node t sits
+ *           at position lengths[b] + depth(t) and sees a committed token or ancestor at
+ *           position u only if u > its position - window or u < sinks
+ *   q       device [B, Hq, T, D] bf16, element strides of (b, h, t) in q_strides (host),
+ *           contiguous head dimension, 16-byte aligned rows
+ *   out     device [B, Hq, T, D] bf16 (contiguous), lse [B, Hq, T] fp32 (natural log)
+ *   workspace >= ring_attn_tree_workspace_bytes(); one call at a time may use it
+ * 1 <= T <= 64, Hq % Hkv == 0. A negative length, a count outside [0, T] or rows past the
+ * capacity make that sequence's rows 0 and -inf, and a parent outside [-1, j) counts as -1;
+ * both are reported as RING_ATTN_EINVAL by ring_attn_status. Rows that no node can see
+ * (behind the last node, or below the window) are not read and may hold anything; every
+ * other row must be finite. A block whose scale is above 2^63 counts as NaN. Results do
+ * not depend on timing: the same call gives the same bits.
+ */
+size_t ring_attn_tree_workspace_bytes(int format, int B, int Hq, int Hkv, int64_t capacity, int D, int T);
+int ring_attn_tree(const void* q, const int64_t* q_strides, const void* k_cache, const void* v_cache,
+                   const void* k_scale, const void* v_scale, int format, void* out, float* lse,
+                   int B, int Hq, int Hkv, int64_t capacity, int D, int T,
+                   const int32_t* lengths, const int32_t* parents, const int32_t* counts,
+                   int window, int sinks, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronise `stream` and read the status word at the start of `workspace`
  * (written by the last compute call that used it): 0, or RING_ATTN_ETIMEOUT.
  * Returns RING_ATTN_ECUDA if the stream reports an error.

@@ -24,3 +24,13 @@ from .backward import (  # noqa: F401
     ring_attention_backward_online,
 )
 from .decode import decode_reference, decode_split  # noqa: F401
+from .serving import (  # noqa: F401
+    element_values,
+    masked_attention,
+    quantise,
+    tree_reference,
+    tree_visible,
+    window_backward_reference,
+    window_reference,
+    window_visible,
+)

@@ -31,6 +31,9 @@ ALGO_TCGEN05 = 2
 ALGO_TCGEN05_1SM = 3
 STEP_FIRST = 1
 STEP_LAST = 2
+CACHE_BF16 = 0
+CACHE_MXFP8 = 1
+CACHE_MXFP4 = 2
 BWD_PART_KV = 1
 BWD_PART_Q = 2
 
@@ -67,6 +70,13 @@ SIGNATURES = {
     "ring_attn_decode_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_int]),
     "ring_attn_decode": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_i64, _c_int, _c_int, _c_int,
                                   _c_float, _c_int, _vp, _c_size, _vp]),
+    "ring_attn_cache_write": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_i64, _c_int,
+                                       _c_int, _c_int, _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "ring_attn_cache_read": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_i64, _c_int, _c_int, _vp, _vp,
+                                      _vp, _vp, _c_int, _vp]),
+    "ring_attn_tree_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_i64, _c_int, _c_int]),
+    "ring_attn_tree": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_i64, _c_int,
+                                _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_float, _vp, _c_size, _vp]),
     "ring_attn_debug_bwd_visit_counts": (_c_i64, [_c_i64, _c_int, _c_int, _c_int, _c_int, _vp]),
     "ring_attn_fwd_noalloc": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_i64, _c_int, _c_int,
                                        _c_int, _c_int, _c_float, _c_int, _vp, ctypes.POINTER(_vp)]),
@@ -198,6 +208,36 @@ def ring_attn_decode(q, k, v, out, lse, B, Hq, Hkv, S, D, P, layout, scale, dtyp
                      stream) -> int:
     return load().ring_attn_decode(q, k, v, out, lse, B, Hq, Hkv, S, D, P, layout, scale, dtype, workspace,
                                    workspace_bytes, stream)
+
+
+def _strides(values):
+    return (_c_i64 * len(values))(*values)
+
+
+def ring_attn_cache_write(k_new, v_new, strides, dtype, k_cache, v_cache, k_scale, v_scale, format_, B, Hkv, capacity,
+                          D, T, T_src, start, count, index, workspace, workspace_bytes, stream) -> int:
+    """strides: six element strides, (b, h, t) of k_new and of v_new."""
+    return load().ring_attn_cache_write(k_new, v_new, _strides(strides), dtype, k_cache, v_cache, k_scale, v_scale,
+                                        format_, B, Hkv, capacity, D, T, T_src, start, count, index, workspace,
+                                        workspace_bytes, stream)
+
+
+def ring_attn_cache_read(k_cache, v_cache, k_scale, v_scale, format_, B, Hkv, capacity, D, T, start, count, k_out,
+                         v_out, dtype, stream) -> int:
+    return load().ring_attn_cache_read(k_cache, v_cache, k_scale, v_scale, format_, B, Hkv, capacity, D, T, start,
+                                       count, k_out, v_out, dtype, stream)
+
+
+def ring_attn_tree_workspace_bytes(format_, B, Hq, Hkv, capacity, D, T) -> int:
+    return load().ring_attn_tree_workspace_bytes(format_, B, Hq, Hkv, capacity, D, T)
+
+
+def ring_attn_tree(q, q_strides, k_cache, v_cache, k_scale, v_scale, format_, out, lse, B, Hq, Hkv, capacity, D, T,
+                   lengths, parents, counts, window, sinks, scale, workspace, workspace_bytes, stream) -> int:
+    """q_strides: three element strides, (b, h, t)."""
+    return load().ring_attn_tree(q, _strides(q_strides), k_cache, v_cache, k_scale, v_scale, format_, out, lse, B, Hq,
+                                 Hkv, capacity, D, T, lengths, parents, counts, window, sinks, scale, workspace,
+                                 workspace_bytes, stream)
 
 
 def ring_attn_debug_bwd_visit_counts(S, P, causal, layout, pass_, counts) -> int:

@@ -1,0 +1,220 @@
+"""A serving cache in fewer bits, and attention of drafted tokens over it.
+
+Marshalling over the C ABI, as in api.py: tensors are checked, outputs allocated with
+torch, and the library's kernels do every step of the computation.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import binding as _b
+from .api import _DTYPES, _stream_ptr
+
+_FORMATS = {"bf16": _b.CACHE_BF16, "mxfp8": _b.CACHE_MXFP8, "mxfp4": _b.CACHE_MXFP4}
+_BLOCK = 32
+
+
+def _code_width(D: int, format: str) -> int:
+    return D // 2 if format == "mxfp4" else D
+
+
+class KVCache:
+    """Rows of K and V for B sequences in one format.
+
+    format "bf16": k, v [B, Hkv, capacity, D] bfloat16. "mxfp8": uint8 e4m3 codes
+    [B, Hkv, capacity, D]; "mxfp4": two e2m1 codes per byte [B, Hkv, capacity, D/2]; both
+    with k_scale, v_scale uint8 [B, Hkv, capacity, D/32] (the byte is the scale's exponent
+    + 127). capacity is a multiple of 16. The tensors are the caller's: nothing is copied.
+    """
+
+    def __init__(self, format: str, k, v, k_scale=None, v_scale=None):
+        if format not in _FORMATS:
+            raise ValueError(f"format must be one of {sorted(_FORMATS)}")
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must be [B, Hkv, capacity, width] tensors of one shape")
+        want = torch.bfloat16 if format == "bf16" else torch.uint8
+        tensors = [k, v] if format == "bf16" else [k, v, k_scale, v_scale]
+        self.D = k.shape[3] * (2 if format == "mxfp4" else 1)
+        if format != "bf16":
+            shape = (*k.shape[:3], self.D // _BLOCK)
+            for s in (k_scale, v_scale):
+                if s is None or tuple(s.shape) != shape or s.dtype != torch.uint8:
+                    raise ValueError("k_scale and v_scale must be uint8 [B, Hkv, capacity, D/32]")
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache has no scales")
+        if k.dtype != want or v.dtype != want:
+            raise ValueError(f"a {format} cache keeps its rows as {want}")
+        if any(t.device != k.device for t in tensors):
+            raise ValueError("the cache's tensors must be on one device")
+        if not all(t.is_contiguous() for t in tensors):
+            raise ValueError("the cache's tensors must be contiguous")
+        self.format, self.k, self.v, self.k_scale, self.v_scale = format, k, v, k_scale, v_scale
+        self.B, self.Hkv, self.capacity = k.shape[:3]
+
+    @classmethod
+    def allocate(cls, B: int, Hkv: int, capacity: int, D: int, format: str = "mxfp8", device="cuda") -> "KVCache":
+        """A cache of uninitialised rows (capacity is rounded up to a multiple of 16)."""
+        if format not in _FORMATS:
+            raise ValueError(f"format must be one of {sorted(_FORMATS)}")
+        if D not in (64, 128):
+            raise ValueError("D must be 64 or 128")
+        cap = (capacity + 15) // 16 * 16
+        if format == "bf16":
+            return cls(format, *(torch.empty(B, Hkv, cap, D, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        rows = [torch.empty(B, Hkv, cap, _code_width(D, format), dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.empty(B, Hkv, cap, D // _BLOCK, dtype=torch.uint8, device=device) for _ in range(2)]
+        return cls(format, *rows, *scales)
+
+    def bytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scale, self.v_scale) if t is not None)
+
+    def _pointers(self):
+        return tuple(0 if t is None else t.data_ptr() for t in (self.k, self.v, self.k_scale, self.v_scale))
+
+
+def _int_rows(t, shape, name, device, optional=True) -> int:
+    if t is None:
+        if optional:
+            return 0
+        raise ValueError(f"{name} is required")
+    if tuple(t.shape) != tuple(shape) or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on the cache's device")
+    return t.data_ptr()
+
+
+def _strides(t):
+    """Element strides of the first three dimensions (those of size 1 do not matter)."""
+    return tuple(s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape[:3]))
+
+
+def _on_device(cache: KVCache):
+    if cache.k.device.type != "cuda":
+        raise ValueError("the cache must be on a CUDA device")
+    return cache.k.device
+
+
+def _stream_of(stream, device) -> int:
+    if stream is None:
+        return int(torch.cuda.current_stream(device).cuda_stream)
+    return _stream_ptr(stream)
+
+
+def cache_write(cache: KVCache, k_new, v_new, start, count=None, index=None, workspace=None, stream=None) -> None:
+    """Write new rows into the cache in its format.
+
+    k_new, v_new [B, Hkv, T, D] bf16 or fp32 with any strides that keep rows 16-byte
+    aligned and the head dimension contiguous (a slice of a fused projection is fine).
+    Cache row start[b] + i becomes new row i for i < count[b] (default: all T). With
+    index [B, n] int32 there are n rows to write and row i comes from new row index[b, i].
+    No other row is touched; rows that would fall outside the cache are skipped, which
+    `status` reports for a given `workspace` (uint8, >= 256 bytes). Asynchronous on `stream`.
+    """
+    dev = _on_device(cache)
+    for t in (k_new, v_new):
+        if t.dim() != 4 or tuple(t.shape[:2]) != (cache.B, cache.Hkv) or t.shape[3] != cache.D:
+            raise ValueError("k_new and v_new must be [B, Hkv, T, D] like the cache")
+        if t.dtype not in _DTYPES or t.dtype != k_new.dtype or t.device != dev:
+            raise ValueError("k_new and v_new must share dtype float32 or bfloat16 and the cache's device")
+        if t.stride(3) != 1:
+            raise ValueError("the head dimension of k_new and v_new must be contiguous")
+    if k_new.shape != v_new.shape:
+        raise ValueError("k_new and v_new must have one shape")
+    T_src = k_new.shape[2]
+    T = T_src if index is None else index.shape[-1]
+    if T == 0 or T_src == 0:
+        return
+    p_start = _int_rows(start, (cache.B,), "start", dev, optional=False)
+    p_count = _int_rows(count, (cache.B,), "count", dev)
+    p_index = _int_rows(index, (cache.B, T), "index", dev)
+    with torch.cuda.device(dev):
+        rc = _b.ring_attn_cache_write(k_new.data_ptr(), v_new.data_ptr(), (*_strides(k_new), *_strides(v_new)),
+                                      _DTYPES[k_new.dtype], *cache._pointers(), _FORMATS[cache.format], cache.B,
+                                      cache.Hkv, cache.capacity, cache.D, T, T_src, p_start, p_count, p_index,
+                                      0 if workspace is None else workspace.data_ptr(),
+                                      0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                      _stream_of(stream, dev))
+    _b.check(rc, "ring_attn_cache_write")
+
+
+def cache_read(cache: KVCache, start, T: int, count=None, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+    """Read rows [start[b], start[b] + T) back as the values they stand for.
+
+    Returns (k, v) [B, Hkv, T, D] in dtype (bf16 or fp32); rows i >= count[b] and rows
+    outside the cache are zeros. Asynchronous on `stream`.
+    """
+    dev = _on_device(cache)
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float32 or bfloat16")
+    shape = (cache.B, cache.Hkv, T, cache.D)
+    outs = []
+    for t in (k_out, v_out):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        elif tuple(t.shape) != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+            raise ValueError("k_out and v_out must be contiguous [B, Hkv, T, D] tensors of dtype")
+        outs.append(t)
+    if T == 0:
+        return tuple(outs)
+    p_start = _int_rows(start, (cache.B,), "start", dev, optional=False)
+    p_count = _int_rows(count, (cache.B,), "count", dev)
+    with torch.cuda.device(dev):
+        rc = _b.ring_attn_cache_read(*cache._pointers(), _FORMATS[cache.format], cache.B, cache.Hkv, cache.capacity,
+                                     cache.D, T, p_start, p_count, outs[0].data_ptr(), outs[1].data_ptr(),
+                                     _DTYPES[dtype], _stream_of(stream, dev))
+    _b.check(rc, "ring_attn_cache_read")
+    return tuple(outs)
+
+
+def tree_workspace(q, cache: KVCache) -> torch.Tensor:
+    """Scratch for tree_attention calls of q's shape over this cache (one call at a time)."""
+    B, Hq, T, D = q.shape
+    n = _b.ring_attn_tree_workspace_bytes(_FORMATS[cache.format], B, Hq, cache.Hkv, cache.capacity, D, T)
+    if n == 0:
+        raise _b.RingAttnError(_b.EINVAL, "ring_attn_tree_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=cache.k.device)
+
+
+def tree_attention(q, cache: KVCache, lengths, parents=None, counts=None, window: int = 0, sinks: int = 0,
+                   scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of T drafted tokens per sequence over its cache (T = 1: ordinary decoding).
+
+    q [B, Hq, T, D] bf16 (rows 16-byte aligned, any other strides). Sequence b holds
+    lengths[b] committed rows; its drafted node j has been written to cache row
+    lengths[b] + j. parents [B, T] int32 gives the tree (parent in [-1, j), -1 the last
+    committed token; None: a chain). Node t sees all committed tokens, its ancestors and
+    itself, or, with window > 0, of these the last `window` positions up to its own
+    (lengths[b] + its depth) and the first `sinks`. counts [B] gives the live nodes; rows of
+    dead ones are 0 with lse = -inf. Returns (out [B, Hq, T, D] bf16, lse [B, Hq, T] fp32).
+    Asynchronous on `stream`.
+    """
+    dev = _on_device(cache)
+    if q.dim() != 4 or q.shape[0] != cache.B or q.shape[3] != cache.D:
+        raise ValueError("q must be [B, Hq, T, D] like the cache")
+    if q.dtype != torch.bfloat16 or q.device != dev or q.stride(3) != 1:
+        raise ValueError("q must be a bf16 tensor on the cache's device with a contiguous head dimension")
+    B, Hq, T, D = q.shape
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    if out is None:
+        out = torch.empty((B, Hq, T, D), dtype=torch.bfloat16, device=dev)
+    elif tuple(out.shape) != (B, Hq, T, D) or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous bf16 [B, Hq, T, D] tensor")
+    if lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+    elif tuple(lse.shape) != (B, Hq, T) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
+        raise ValueError("lse must be a contiguous float32 [B, Hq, T] tensor")
+    p_len = _int_rows(lengths, (B,), "lengths", dev, optional=False)
+    p_par = _int_rows(parents, (B, T), "parents", dev)
+    p_cnt = _int_rows(counts, (B,), "counts", dev)
+    if workspace is None:
+        workspace = tree_workspace(q, cache)
+    elif workspace.device != dev:
+        raise ValueError("workspace must be on the cache's device")
+    with torch.cuda.device(dev):
+        rc = _b.ring_attn_tree(q.data_ptr(), _strides(q), *cache._pointers(), _FORMATS[cache.format],
+                               out.data_ptr(), lse.data_ptr(), B, Hq, cache.Hkv, cache.capacity, D, T, p_len, p_par,
+                               p_cnt, int(window), int(sinks), scale, workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _stream_of(stream, dev))
+    _b.check(rc, "ring_attn_tree")
+    return out, lse

@@ -359,6 +359,106 @@ int ring_attn_decode(const void* q, const void* k, const void* v, void* out, flo
                              watchdog_ns(), st);
 }
 
+namespace {
+
+// Row strides in elements are multiples of 16 bytes, so every row of a view stays aligned.
+bool strides_aligned(const int64_t* s, int n, int elem_bytes) {
+  for (int i = 0; i < n; ++i)
+    if ((s[i] * elem_bytes) % 16 != 0) return false;
+  return true;
+}
+
+int check_cache(const void* k, const void* v, const void* ks, const void* vs, int format, int B, int Hkv,
+                int64_t capacity, int D, CacheView* c) {
+  if (format != RING_ATTN_CACHE_BF16 && format != RING_ATTN_CACHE_MXFP8 && format != RING_ATTN_CACHE_MXFP4)
+    return RING_ATTN_EINVAL;
+  if (B <= 0 || Hkv <= 0 || D <= 0 || capacity <= 0 || capacity > ((int64_t)1 << 30) || capacity % 16 != 0)
+    return RING_ATTN_EINVAL;
+  if (D != 64 && D != 128) return RING_ATTN_EUNSUPPORTED;
+  if ((int64_t)B * Hkv > (1 << 24)) return RING_ATTN_EINVAL;
+  if (!k || !v) return RING_ATTN_EINVAL;
+  if (format != RING_ATTN_CACHE_BF16 && (!ks || !vs)) return RING_ATTN_EINVAL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(ks) || !aligned16(vs)) return RING_ATTN_EALIGN;
+  c->k = const_cast<void*>(k);
+  c->v = const_cast<void*>(v);
+  c->k_scale = const_cast<void*>(ks);
+  c->v_scale = const_cast<void*>(vs);
+  c->format = format;
+  c->B = B;
+  c->Hkv = Hkv;
+  c->D = D;
+  c->capacity = capacity;
+  return RING_ATTN_OK;
+}
+
+bool rows_fit(int B, int Hkv, int T) { return 2ll * B * Hkv * T < ((int64_t)1 << 31); }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+int ring_attn_cache_write(const void* k_new, const void* v_new, const int64_t* strides, int dtype, void* k_cache,
+                          void* v_cache, void* k_scale, void* v_scale, int format, int B, int Hkv, int64_t capacity,
+                          int D, int T, int T_src, const int32_t* start, const int32_t* count, const int32_t* index,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  CacheView c;
+  int rc = check_cache(k_cache, v_cache, k_scale, v_scale, format, B, Hkv, capacity, D, &c);
+  if (rc) return rc;
+  if (dtype != RING_ATTN_DTYPE_FP32 && dtype != RING_ATTN_DTYPE_BF16) return RING_ATTN_EINVAL;
+  if (!k_new || !v_new || !strides || !start || T <= 0 || T_src <= 0 || !rows_fit(B, Hkv, T)) return RING_ATTN_EINVAL;
+  if (!index && T_src < T) return RING_ATTN_EINVAL;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned4(start) || !aligned4(count) || !aligned4(index) ||
+      !strides_aligned(strides, 6, dtype == RING_ATTN_DTYPE_BF16 ? 2 : 4))
+    return RING_ATTN_EALIGN;
+  if (workspace && (workspace_bytes < kWorkspaceHeaderBytes || !aligned16(workspace))) return RING_ATTN_EWORKSPACE;
+  if (!device_is_sm100()) return RING_ATTN_EUNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (workspace && (rc = reset_status(workspace, st))) return rc;
+  return launch_cache_write(c, k_new, v_new, strides, dtype, T, T_src, start, count, index,
+                            static_cast<int*>(workspace), st);
+}
+
+int ring_attn_cache_read(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                         int format, int B, int Hkv, int64_t capacity, int D, int T, const int32_t* start,
+                         const int32_t* count, void* k_out, void* v_out, int dtype, void* stream) {
+  CacheView c;
+  int rc = check_cache(k_cache, v_cache, k_scale, v_scale, format, B, Hkv, capacity, D, &c);
+  if (rc) return rc;
+  if (dtype != RING_ATTN_DTYPE_FP32 && dtype != RING_ATTN_DTYPE_BF16) return RING_ATTN_EINVAL;
+  if (!k_out || !v_out || !start || T <= 0 || !rows_fit(B, Hkv, T)) return RING_ATTN_EINVAL;
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned4(start) || !aligned4(count)) return RING_ATTN_EALIGN;
+  if (!device_is_sm100()) return RING_ATTN_EUNSUPPORTED;
+  return launch_cache_read(c, T, start, count, k_out, v_out, dtype, static_cast<cudaStream_t>(stream));
+}
+
+size_t ring_attn_tree_workspace_bytes(int format, int B, int Hq, int Hkv, int64_t capacity, int D, int T) {
+  CacheView c;
+  const void* some = reinterpret_cast<const void*>(uintptr_t(256));  // only the sizes are looked at
+  if (check_cache(some, some, some, some, format, B, Hkv, capacity, D, &c) != RING_ATTN_OK) return 0;
+  if (Hq <= 0 || Hq % Hkv != 0 || T < 1 || T > 64 || (int64_t)B * Hq > (1 << 24)) return 0;
+  return tree_workspace_bytes(c, Hq, T);
+}
+
+int ring_attn_tree(const void* q, const int64_t* q_strides, const void* k_cache, const void* v_cache,
+                   const void* k_scale, const void* v_scale, int format, void* out, float* lse, int B, int Hq,
+                   int Hkv, int64_t capacity, int D, int T, const int32_t* lengths, const int32_t* parents,
+                   const int32_t* counts, int window, int sinks, float scale, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  CacheView c;
+  int rc = check_cache(k_cache, v_cache, k_scale, v_scale, format, B, Hkv, capacity, D, &c);
+  if (rc) return rc;
+  if (Hq <= 0 || Hq % Hkv != 0 || T < 1 || T > 64 || (int64_t)B * Hq > (1 << 24)) return RING_ATTN_EINVAL;
+  if (!q || !q_strides || !out || !lse || !lengths || window < 0 || sinks < 0) return RING_ATTN_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || !aligned4(lse) || !aligned4(lengths) || !aligned4(parents) ||
+      !aligned4(counts) || !strides_aligned(q_strides, 3, 2))
+    return RING_ATTN_EALIGN;
+  if (!(scale > 0.f) || !isfinite(scale)) return RING_ATTN_EINVAL;
+  if (!workspace || workspace_bytes < tree_workspace_bytes(c, Hq, T) || !aligned16(workspace))
+    return RING_ATTN_EWORKSPACE;
+  if (!device_is_sm100()) return RING_ATTN_EUNSUPPORTED;
+  return launch_tree(c, q, q_strides, out, lse, lengths, parents, counts, Hq, T, window, sinks, scale, workspace,
+                     watchdog_ns(), static_cast<cudaStream_t>(stream));
+}
+
 int ring_attn_status(const void* workspace, void* stream) {
   if (!workspace) return RING_ATTN_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -1,0 +1,320 @@
+// Writing rows of K and V into a cache in its format, and reading them back.
+//
+// Both are bound by HBM: a write reads the new rows once and writes codes and scales
+// once, a read the other way round. A thread owns 8 consecutive elements of a row on the
+// write side (one 16-byte load of bf16, 8 or 4 bytes of codes out), so the 32 values of
+// a scale block sit in 4 neighbouring lanes and their maximum takes two shuffles; on the
+// read side it owns the elements of one 16-byte store. K and V rows go through one
+// launch.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mx_format.cuh"
+#include "ringattn_internal.h"
+
+namespace ringattn {
+namespace cache {
+
+constexpr int kThreads = 256;
+
+struct WriteParams {
+  const void* src[2];      // k_new, v_new
+  int64_t stride[2][3];    // (b, h, t) in elements
+  uint8_t* codes[2];
+  uint8_t* scale[2];
+  const int32_t* start;    // [B]
+  const int32_t* count;    // [B] or null
+  const int32_t* index;    // [B, T] or null
+  int B, Hkv, T, T_src;
+  int64_t capacity;
+  uint32_t rows;           // 2 * B * Hkv * T
+  int* status;             // or null
+};
+
+struct ReadParams {
+  const uint8_t* codes[2];
+  const uint8_t* scale[2];
+  void* out[2];            // [B, Hkv, T, D]
+  const int32_t* start;
+  const int32_t* count;
+  int B, Hkv, T;
+  int64_t capacity;
+  uint32_t rows;
+};
+
+// K's or V's pointer, by a select (an index into the parameters would copy them to the stack)
+template <typename P>
+__device__ __forceinline__ P pick(P const (&a)[2], int which) {
+  return which ? a[1] : a[0];
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// kRows rows per thread, their loads issued before any of them is encoded.
+template <int FMT, int D, typename T, int kRows>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteParams p) {
+  constexpr int kTpr = D / 8;                   // threads per row
+  constexpr int kRpb = kThreads / kTpr;         // rows per block and step
+  const int sub = threadIdx.x % kTpr;
+  float x[kRows][8];
+  int64_t dst[kRows];
+  int which[kRows];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const uint32_t r = (blockIdx.x * kRows + u) * (uint32_t)kRpb + threadIdx.x / kTpr;
+    dst[u] = -1;
+    which[u] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
+    if (r >= p.rows) continue;
+    const uint32_t i = r % (uint32_t)p.T;
+    uint32_t y = r / (uint32_t)p.T;
+    const uint32_t h = y % (uint32_t)p.Hkv;
+    y /= (uint32_t)p.Hkv;
+    const uint32_t b = y % (uint32_t)p.B;
+    which[u] = (int)(y / (uint32_t)p.B);
+    const int32_t n = p.count ? p.count[b] : p.T;
+    if ((int32_t)i >= n) continue;
+    const int64_t pos = (int64_t)p.start[b] + i;
+    const int64_t from = p.index ? (int64_t)p.index[(int64_t)b * p.T + i] : (int64_t)i;
+    if (pos < 0 || pos >= p.capacity || from < 0 || from >= p.T_src || n > p.T) {
+      if (p.status && sub == 0) atomicExch(p.status, RING_ATTN_EINVAL);
+      if (pos < 0 || pos >= p.capacity || from < 0 || from >= p.T_src) continue;
+    }
+    const bool w = which[u] != 0;
+    const int64_t off = b * (w ? p.stride[1][0] : p.stride[0][0]) + h * (w ? p.stride[1][1] : p.stride[0][1]) +
+                        from * (w ? p.stride[1][2] : p.stride[0][2]);
+    load8(static_cast<const T*>(pick(p.src, w)) + off + sub * 8, x[u]);
+    dst[u] = ((int64_t)b * p.Hkv + h) * p.capacity + pos;
+  }
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    if (FMT == RING_ATTN_CACHE_BF16) {
+      if (dst[u] < 0) continue;
+      uint4 o;
+      o.x = bf16_pair(x[u][0], x[u][1]);
+      o.y = bf16_pair(x[u][2], x[u][3]);
+      o.z = bf16_pair(x[u][4], x[u][5]);
+      o.w = bf16_pair(x[u][6], x[u][7]);
+      *reinterpret_cast<uint4*>(pick(p.codes, which[u]) + dst[u] * (2 * D) + sub * 16) = o;
+      continue;
+    }
+    // the block's largest magnitude as fp32 bits: an unsigned maximum, so a NaN is kept
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t a = __float_as_uint(x[u][e]) & 0x7fffffffu;
+      m = a > m ? a : m;
+    }
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (dst[u] < 0) continue;
+    const uint32_t byte = mx_scale_byte<FMT>(m);
+    const float inv = byte == 255u ? 0.f : mx_inverse_scale(byte);
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = byte == 255u ? 0.f : x[u][e] * inv;
+    if (FMT == RING_ATTN_CACHE_MXFP8) {
+      uint2 o;
+      o.x = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
+      o.y = e4m3_pair(y[4], y[5]) | (e4m3_pair(y[6], y[7]) << 16);
+      *reinterpret_cast<uint2*>(pick(p.codes, which[u]) + dst[u] * D + sub * 8) = o;
+    } else {
+      const uint32_t o = e2m1_pair(y[0], y[1]) | (e2m1_pair(y[2], y[3]) << 8) | (e2m1_pair(y[4], y[5]) << 16) |
+                         (e2m1_pair(y[6], y[7]) << 24);
+      *reinterpret_cast<uint32_t*>(pick(p.codes, which[u]) + dst[u] * (D / 2) + sub * 4) = o;
+    }
+    if (sub % 4 == 0) pick(p.scale, which[u])[dst[u] * (D / kMxBlock) + sub / 4] = (uint8_t)byte;
+  }
+}
+
+template <int FMT, int D, typename T, int kRows>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p) {
+  constexpr int kEl = 16 / (int)sizeof(T);      // elements per thread: one 16-byte store
+  constexpr int kTpr = D / kEl;
+  constexpr int kRpb = kThreads / kTpr;
+  constexpr int kBytes = FMT == RING_ATTN_CACHE_BF16 ? 2 * kEl : (FMT == RING_ATTN_CACHE_MXFP8 ? kEl : kEl / 2);
+  const int sub = threadIdx.x % kTpr;
+  uint32_t c[kRows][(kBytes + 3) / 4];
+  uint32_t s[kRows];
+  int64_t out_row[kRows];
+  int which[kRows];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const uint32_t r = (blockIdx.x * kRows + u) * (uint32_t)kRpb + threadIdx.x / kTpr;
+    out_row[u] = -1;
+    which[u] = 0;
+    s[u] = 0;
+#pragma unroll
+    for (int e = 0; e < (kBytes + 3) / 4; ++e) c[u][e] = 0u;
+    if (r >= p.rows) continue;
+    const uint32_t i = r % (uint32_t)p.T;
+    uint32_t y = r / (uint32_t)p.T;
+    const uint32_t h = y % (uint32_t)p.Hkv;
+    y /= (uint32_t)p.Hkv;
+    const uint32_t b = y % (uint32_t)p.B;
+    which[u] = (int)(y / (uint32_t)p.B);
+    out_row[u] = (int64_t)(r % (p.rows / 2));
+    // rows past the count, or outside the cache, read as zeros
+    if (p.count && (int32_t)i >= p.count[b]) continue;
+    const int64_t pos = (int64_t)p.start[b] + i;
+    if (pos < 0 || pos >= p.capacity) continue;
+    const int64_t row = ((int64_t)b * p.Hkv + h) * p.capacity + pos;
+    const uint8_t* q = pick(p.codes, which[u]) + row * cache_row_bytes<FMT>(D) + sub * kBytes;
+    if constexpr (kBytes == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(q);
+      c[u][0] = v.x; c[u][1] = v.y; c[u][2] = v.z; c[u][3] = v.w;
+    } else if constexpr (kBytes == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(q);
+      c[u][0] = v.x; c[u][1] = v.y;
+    } else if constexpr (kBytes == 4) {
+      c[u][0] = *reinterpret_cast<const uint32_t*>(q);
+    } else {
+      c[u][0] = *reinterpret_cast<const uint16_t*>(q);
+    }
+    if (FMT != RING_ATTN_CACHE_BF16) s[u] = pick(p.scale, which[u])[row * (D / kMxBlock) + sub * kEl / kMxBlock];
+  }
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    if (out_row[u] < 0) continue;
+    float x[kEl];
+    const float f = FMT == RING_ATTN_CACHE_BF16 ? 1.f : mx_scale(s[u]);
+#pragma unroll
+    for (int e = 0; e < kEl; e += 2) {
+      float2 v;
+      if (FMT == RING_ATTN_CACHE_BF16) {
+        v = make_float2(__uint_as_float(c[u][e / 2] << 16), __uint_as_float(c[u][e / 2] & 0xffff0000u));
+      } else if (FMT == RING_ATTN_CACHE_MXFP8) {
+        v = e4m3_values(c[u][e / 4] >> (8 * (e % 4)));
+      } else {
+        v = e2m1_values(c[u][e / 8] >> (4 * (e % 8)));
+      }
+      x[e] = FMT == RING_ATTN_CACHE_BF16 ? v.x : v.x * f;
+      x[e + 1] = FMT == RING_ATTN_CACHE_BF16 ? v.y : v.y * f;
+    }
+    T* o = static_cast<T*>(pick(p.out, which[u])) + out_row[u] * D + sub * kEl;
+    uint4 w;
+    if constexpr (sizeof(T) == 2) {
+      w = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+    } else {
+      w = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+    *reinterpret_cast<uint4*>(o) = w;
+  }
+}
+
+// Rows per thread: 4 where that still leaves every SM its 8 resident blocks, else 1
+// (a single token's append is one short wave either way).
+inline int rows_per_thread(uint32_t rows, int rpb) { return rows >= 4ull * 8 * 148 * rpb ? 4 : 1; }
+
+inline unsigned blocks_for(uint32_t rows, int rpb, int per) {
+  const uint64_t n = (uint64_t)rpb * per;
+  return (unsigned)((rows + n - 1) / n);
+}
+
+template <int FMT, int D, typename T>
+int write_t(const WriteParams& p, cudaStream_t stream) {
+  constexpr int rpb = kThreads / (D / 8);
+  if (rows_per_thread(p.rows, rpb) == 4)
+    cache_write_kernel<FMT, D, T, 4><<<blocks_for(p.rows, rpb, 4), kThreads, 0, stream>>>(p);
+  else
+    cache_write_kernel<FMT, D, T, 1><<<blocks_for(p.rows, rpb, 1), kThreads, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
+}
+
+template <int FMT, int D, typename T>
+int read_t(const ReadParams& p, cudaStream_t stream) {
+  constexpr int rpb = kThreads / (D * (int)sizeof(T) / 16);
+  if (rows_per_thread(p.rows, rpb) == 4)
+    cache_read_kernel<FMT, D, T, 4><<<blocks_for(p.rows, rpb, 4), kThreads, 0, stream>>>(p);
+  else
+    cache_read_kernel<FMT, D, T, 1><<<blocks_for(p.rows, rpb, 1), kThreads, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
+}
+
+template <int FMT>
+int write_f(const WriteParams& p, int D, int dtype, cudaStream_t s) {
+  if (dtype == RING_ATTN_DTYPE_BF16)
+    return D == 64 ? write_t<FMT, 64, __nv_bfloat16>(p, s) : write_t<FMT, 128, __nv_bfloat16>(p, s);
+  return D == 64 ? write_t<FMT, 64, float>(p, s) : write_t<FMT, 128, float>(p, s);
+}
+
+template <int FMT>
+int read_f(const ReadParams& p, int D, int dtype, cudaStream_t s) {
+  if (dtype == RING_ATTN_DTYPE_BF16)
+    return D == 64 ? read_t<FMT, 64, __nv_bfloat16>(p, s) : read_t<FMT, 128, __nv_bfloat16>(p, s);
+  return D == 64 ? read_t<FMT, 64, float>(p, s) : read_t<FMT, 128, float>(p, s);
+}
+
+}  // namespace cache
+
+int launch_cache_write(const CacheView& c, const void* k_new, const void* v_new, const int64_t* strides, int dtype,
+                       int T, int T_src, const int32_t* start, const int32_t* count, const int32_t* index,
+                       int* status, cudaStream_t stream) {
+  cache::WriteParams p;
+  p.src[0] = k_new;
+  p.src[1] = v_new;
+  for (int i = 0; i < 2; ++i) {
+    for (int x = 0; x < 3; ++x) p.stride[i][x] = strides[3 * i + x];
+    p.codes[i] = static_cast<uint8_t*>(i == 0 ? c.k : c.v);
+    p.scale[i] = static_cast<uint8_t*>(i == 0 ? c.k_scale : c.v_scale);
+  }
+  p.start = start;
+  p.count = count;
+  p.index = index;
+  p.B = c.B;
+  p.Hkv = c.Hkv;
+  p.T = T;
+  p.T_src = T_src;
+  p.capacity = c.capacity;
+  p.rows = (uint32_t)(2ll * c.B * c.Hkv * T);
+  p.status = status;
+  switch (c.format) {
+    case RING_ATTN_CACHE_BF16: return cache::write_f<RING_ATTN_CACHE_BF16>(p, c.D, dtype, stream);
+    case RING_ATTN_CACHE_MXFP8: return cache::write_f<RING_ATTN_CACHE_MXFP8>(p, c.D, dtype, stream);
+    default: return cache::write_f<RING_ATTN_CACHE_MXFP4>(p, c.D, dtype, stream);
+  }
+}
+
+int launch_cache_read(const CacheView& c, int T, const int32_t* start, const int32_t* count, void* k_out, void* v_out,
+                      int dtype, cudaStream_t stream) {
+  cache::ReadParams p;
+  for (int i = 0; i < 2; ++i) {
+    p.codes[i] = static_cast<const uint8_t*>(i == 0 ? c.k : c.v);
+    p.scale[i] = static_cast<const uint8_t*>(i == 0 ? c.k_scale : c.v_scale);
+    p.out[i] = i == 0 ? k_out : v_out;
+  }
+  p.start = start;
+  p.count = count;
+  p.B = c.B;
+  p.Hkv = c.Hkv;
+  p.T = T;
+  p.capacity = c.capacity;
+  p.rows = (uint32_t)(2ll * c.B * c.Hkv * T);
+  switch (c.format) {
+    case RING_ATTN_CACHE_BF16: return cache::read_f<RING_ATTN_CACHE_BF16>(p, c.D, dtype, stream);
+    case RING_ATTN_CACHE_MXFP8: return cache::read_f<RING_ATTN_CACHE_MXFP8>(p, c.D, dtype, stream);
+    default: return cache::read_f<RING_ATTN_CACHE_MXFP4>(p, c.D, dtype, stream);
+  }
+}
+
+}  // namespace ringattn

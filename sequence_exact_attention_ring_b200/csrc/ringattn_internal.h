@@ -98,6 +98,30 @@ int launch_bwd_simt(const void* q, const void* k, const void* v, const void* out
                     void* dq, void* dk, void* dv, const RingGeom& g, float scale, int dtype, float* stats,
                     cudaStream_t stream);
 
+// A key-value cache with its own capacity and format (RING_ATTN_CACHE_*): codes (or bf16
+// rows) [B, Hkv, capacity, D], scale bytes [B, Hkv, capacity, D/32] (null for bf16).
+struct CacheView {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  int format, B, Hkv, D;
+  int64_t capacity;
+};
+
+// strides: (b, h, t) of k_new, then of v_new, in elements. status may be null.
+int launch_cache_write(const CacheView& c, const void* k_new, const void* v_new, const int64_t* strides, int dtype,
+                       int T, int T_src, const int32_t* start, const int32_t* count, const int32_t* index,
+                       int* status, cudaStream_t stream);
+int launch_cache_read(const CacheView& c, int T, const int32_t* start, const int32_t* count, void* k_out, void* v_out,
+                      int dtype, cudaStream_t stream);
+
+// Attention of up to 64 drafted tokens per sequence over a cache.
+size_t tree_workspace_bytes(const CacheView& c, int Hq, int T);
+int launch_tree(const CacheView& c, const void* q, const int64_t* qs, void* out, float* lse, const int32_t* lengths,
+                const int32_t* parents, const int32_t* counts, int Hq, int T, int window, int sinks, float scale,
+                void* workspace, uint64_t watchdog_ns, cudaStream_t stream);
+
 int launch_merge(const float* o_parts, const float* lse_parts, int n_parts, int64_t rows, int D, void* out,
                  float* lse_out, int out_dtype, cudaStream_t stream);
 

@@ -1,0 +1,297 @@
+"""GPU: attention of drafted tokens over a cache, against the fp64 oracle on the cache's values.
+
+Tolerances are counted, per element, from the magnitudes the oracle returns (A = sum p|v|,
+E = scale sum |q||k|): each weight p is rounded to bf16 for its product (2^-8 A), the result
+once more (2^-8 |O| <= 2^-8 A); a score is a sum of D products accumulated in fp32, off by at
+most D 2^-23 E (twice the half-step bound, for a truncating adder), and enters a weight and
+the weights' sum (2 D 2^-23 E A); 2^x is good to 2^-22, sums and rescales to a few 2^-23 (the
+2^-16 covers them at these lengths).
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from sequence_exact_attention_ring_b200 import (KVCache, RingAttnError, binding, cache_read, cache_write, merge, status,
+                                                tree_attention, tree_workspace)
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def check(out, lse, ref, D, what=""):
+    O, L, A, E = ref
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    seen = np.isfinite(L)
+    assert (np.isneginf(l) == ~seen).all(), what
+    assert (o[~seen] == 0).all(), what
+    es = D * 2.0 ** -23 * E + 2.0 ** -16
+    tol = A * (2.0 ** -8 + 2.0 ** -8 + 2 * es[..., None]) + 2.0 ** -126
+    assert np.isfinite(o).all(), what
+    worst = (np.abs(o - O) / tol).max()
+    assert worst <= 1, f"{what}: out off by {worst:.2f} of its tolerance"
+    d = np.abs(l[seen] - L[seen])
+    t = (es + 2.0 ** -22 * (np.abs(np.where(seen, L, 0)) + 4))[seen]
+    assert (d <= t).all(), f"{what}: lse off by {(d / t).max():.2f} of its tolerance"
+
+
+def make(B, Hq, Hkv, D, T, lengths, fmt, seed, cap=None, spread=1.5):
+    g = torch.Generator().manual_seed(seed)
+    cap = cap or (max(lengths) + T + 15) // 16 * 16
+    cache = KVCache.allocate(B, Hkv, cap, D, fmt)
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        if t is not None:
+            t.view(torch.uint8).fill_(0xff)  # rows that are never written read as NaN
+    k = torch.randn(B, Hkv, cap, D, generator=g)
+    v = torch.randn(B, Hkv, cap, D, generator=g) + 0.5
+    k[..., 3::29] *= 4
+    k, v = k.bfloat16().cuda(), v.bfloat16().cuda()
+    for b in range(B):  # committed rows and drafts
+        n = lengths[b] + T
+        one = KVCache(fmt, *(None if t is None else t[b:b + 1] for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+        cache_write(one, k[b:b + 1, :, :n], v[b:b + 1, :, :n], i32([0]))
+    q = (spread * torch.randn(B, T, Hq, D, generator=g)).bfloat16().cuda().transpose(1, 2)
+    vals = [t.double().cpu().numpy() for t in cache_read(cache, i32([0] * B), cap)]
+    return q, cache, vals
+
+
+def random_tree(B, T, seed):
+    r = np.random.default_rng(seed)
+    return [[-1 if i == 0 else int(r.integers(-1, i)) for i in range(T)] for _ in range(B)]
+
+
+def run(q, cache, vals, lengths, parents=None, counts=None, window=0, sinks=0, scale=None, what=""):
+    D = q.shape[-1]
+    ws = tree_workspace(q, cache)
+    out, lse = tree_attention(q, cache, i32(lengths), None if parents is None else i32(parents),
+                              None if counts is None else i32(counts), window, sinks, scale, workspace=ws)
+    assert status(ws) == 0
+    ref = oracle.tree_reference(q.double().cpu().numpy(), *vals, lengths, parents, counts, window, sinks,
+                                1 / np.sqrt(D) if scale is None else scale)
+    check(out, lse, ref, D, what)
+    return out, lse
+
+
+FORMATS = ["bf16", "mxfp8", "mxfp4"]
+SHAPES = [
+    # B, Hq, Hkv, T, lengths
+    (1, 1, 1, 1, [0]),                     # the drafted token alone
+    (1, 2, 2, 1, [1]),
+    (3, 4, 2, 1, [15, 16, 17]),            # around a step's end
+    (2, 8, 1, 1, [700, 0]),                # grouped heads, an empty cache in the batch
+    (2, 4, 4, 3, [64, 63]),
+    (1, 32, 1, 5, [333]),                  # 160 rows: ten row groups
+    (2, 6, 2, 33, [129, 260]),             # 99 rows per kv head: a ragged last group
+    (1, 4, 1, 64, [500]),
+]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s[:4])))
+def test_trees_against_oracle(cuda_lib, fmt, D, shape):
+    B, Hq, Hkv, T, lengths = shape
+    q, cache, vals = make(B, Hq, Hkv, D, T, lengths, fmt, 11)
+    run(q, cache, vals, lengths, random_tree(B, T, 5), what="tree")
+    run(q, cache, vals, lengths, what="chain")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 3), (16, 0), (17, 5), (100, 1), (100, 40), (5000, 3),
+                                          (130, 1000)])
+def test_window_and_sinks(cuda_lib, fmt, window, sinks):
+    """Windows from one position to past the start, also shorter than the drafted tree is deep."""
+    B, T = 3, 21
+    lengths = [401, 3, 96]
+    q, cache, vals = make(B, 4, 2, 128, T, lengths, fmt, 21)
+    run(q, cache, vals, lengths, random_tree(B, T, 6), window=window, sinks=sinks, what="tree")
+    run(q, cache, vals, lengths, window=window, sinks=sinks, what="chain")
+    q1, cache, vals = make(B, 4, 2, 64, 1, lengths, fmt, 22)
+    run(q1, cache, vals, lengths, window=window, sinks=sinks, what="token")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_counts_and_dead_rows(cuda_lib, fmt):
+    """Dead nodes give 0 and -inf; rows behind the last node and rows that fell out of every window hold NaN."""
+    B, T, lengths, counts = 4, 9, [300, 40, 0, 200], [9, 1, 4, 0]
+    q, cache, vals = make(B, 4, 2, 128, T, lengths, fmt, 31, cap=512)
+    for b in range(B):
+        for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+            if t is not None:
+                t[b, :, lengths[b] + counts[b]:].view(torch.uint8).fill_(0xff)
+    run(q, cache, vals, lengths, random_tree(B, T, 7), counts, what="counts")
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        if t is not None:
+            t[0, :, 3:300 - 50 + 1].view(torch.uint8).fill_(0xff)
+    run(q, cache, vals, lengths, random_tree(B, T, 7), counts, window=50, sinks=3, what="evicted rows")
+
+
+def test_large_scores_and_far_scales(cuda_lib):
+    """Scores far apart (one key wins), rising maxima, tiny and large block scales."""
+    for fmt in FORMATS:
+        q, cache, vals = make(2, 4, 2, 128, 4, [600, 77], fmt, 41, spread=40.0)
+        run(q, cache, vals, [600, 77], what="spread " + fmt)
+    g = torch.Generator().manual_seed(9)
+    for fmt in ("mxfp8", "mxfp4"):
+        for e in (-100, -40, 40, 60):
+            cache = KVCache.allocate(1, 1, 64, 64, fmt)
+            k = torch.randn(1, 1, 64, 64, generator=g) * 2.0 ** e
+            v = torch.randn(1, 1, 64, 64, generator=g) * 2.0 ** -e
+            cache_write(cache, k.cuda(), v.cuda(), i32([0]))
+            vals = [t.double().cpu().numpy() for t in cache_read(cache, i32([0]), 64, dtype=torch.float32)]
+            q = (torch.randn(1, 2, 1, 64, generator=g) * (2.0 ** -e if e > -100 else 1.0)).bfloat16().cuda()
+            if e == -100:  # V's scales lie above 2^63: its blocks count as NaN, the scores are as they were
+                out, lse = tree_attention(q, cache, i32([63]))
+                L = oracle.tree_reference(q.double().cpu().numpy(), *vals, [63], None, None, 0, 0, 1 / 8)[1]
+                assert out.isnan().all() and np.abs(lse.double().cpu().numpy() - L).max() <= 2.0 ** -15
+                continue
+            run(q, cache, vals, [63], what=f"{fmt} 2^{e}")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_long_cache_splits_and_repeats(cuda_lib, fmt):
+    """Long enough that every unit is split over many CTAs; ragged; the same bits twice."""
+    lengths = [20011, 333, 8192]
+    q, cache, vals = make(3, 4, 1, 128, 2, lengths, fmt, 51)
+    o1, l1 = run(q, cache, vals, lengths, what="long")
+    o2, l2 = tree_attention(q, cache, i32(lengths))
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+
+
+def test_offsets_past_32_bits(cuda_lib):
+    """A cache of more than 2^32 bytes per tensor: the last sequence's rows lie past a 32-bit offset."""
+    B, Hkv, cap, D = 5, 8, 1 << 20, 128
+    cache = KVCache("mxfp8", *(torch.empty(B, Hkv, cap, D, dtype=torch.uint8, device="cuda") for _ in range(2)),
+                    *(torch.empty(B, Hkv, cap, D // 32, dtype=torch.uint8, device="cuda") for _ in range(2)))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    new = torch.randn(B, Hkv, 80, D, generator=g, device="cuda").bfloat16()
+    start = [0, 0, 0, 0, cap - 80]
+    cache_write(cache, new, -new, i32(start))
+    ko, vo = cache_read(cache, i32(start), 80)
+    assert torch.equal(ko, -vo)
+    want = oracle.quantise(new[4, 7].double().cpu().numpy(), "mxfp8")[2]
+    np.testing.assert_array_equal(ko[4, 7].double().cpu().numpy(), want)
+    # a window over the end of the last sequence's full cache
+    q = torch.randn(B, 8, 1, D, generator=g, device="cuda").bfloat16()
+    lengths = [79, 79, 79, 79, cap - 1]
+    out, lse = tree_attention(q, cache, i32(lengths), window=80)
+    vals = [t.double().cpu().numpy() for t in (ko, vo)]
+    ref = oracle.tree_reference(q.double().cpu().numpy(), *vals, [79] * 5, None, None, 80, 0, 1 / np.sqrt(D))
+    check(out, lse, ref, D)
+
+
+def test_draft_verify_accept(cuda_lib):
+    """The operators as they are used: a prompt's rows, a drafted tree behind them, its attention, the
+    accepted path written over the drafts, the next token; equal to attention over the plain sequence."""
+    B, Hq, Hkv, D, n, T = 2, 4, 2, 128, 200, 6
+    g = torch.Generator().manual_seed(61)
+    for fmt in FORMATS:
+        cache = KVCache.allocate(B, Hkv, 512, D, fmt)
+        prompt = torch.randn(2, B, Hkv, n, D, generator=g).bfloat16().cuda()
+        cache_write(cache, prompt[0], prompt[1], i32([0, 0]))
+        draft = torch.randn(2, B, Hkv, T, D, generator=g).bfloat16().cuda()
+        cache_write(cache, draft[0], draft[1], i32([n, n]))
+        parents = [[-1, 0, 0, 1, 2, 4], [-1, -1, 1, 1, 3, 0]]
+        q = torch.randn(B, Hq, T, D, generator=g).bfloat16().cuda()
+        out, lse = tree_attention(q, cache, i32([n, n]), i32(parents))
+        path, count = [[0, 2, 4], [1, 3, 0]], [3, 2]  # accepted nodes, root first
+        cache_write(cache, draft[0], draft[1], i32([n, n]), count=i32(count), index=i32(path))
+        # each accepted node's row equals plain attention over prompt + path up to it
+        vals = [t.double().cpu().numpy() for t in cache_read(cache, i32([0, 0]), 512)]
+        for b in range(B):
+            for i in range(count[b]):
+                o1, l1, A, E = oracle.tree_reference(q[b:b + 1, :, path[b][i]:path[b][i] + 1].double().cpu().numpy(),
+                                                     *(x[b:b + 1] for x in vals), [n + i], None, None, 0, 0, D ** -0.5)
+                check(out[b:b + 1, :, path[b][i]:path[b][i] + 1], lse[b:b + 1, :, path[b][i]:path[b][i] + 1],
+                      (o1, l1, A, E), D, f"{fmt} {b} {i}")
+        new = torch.randn(2, B, Hkv, 1, D, generator=g).bfloat16().cuda()
+        lengths = [n + c for c in count]
+        cache_write(cache, new[0], new[1], i32(lengths))
+        vals = [t.double().cpu().numpy() for t in cache_read(cache, i32([0, 0]), 512)]
+        run(q[:, :, :1], cache, vals, lengths, what="next token")
+
+
+def test_split_cache_merges(cuda_lib):
+    """Two caches over two halves of the keys: their (out, lse) merge to attention over both."""
+    q, cache, vals = make(1, 4, 2, 128, 1, [300], "mxfp8", 71)
+    whole, lse = tree_attention(q, cache, i32([300]))
+    parts = []
+    for lo, hi in ((0, 160), (160, 301)):
+        half = KVCache.allocate(1, 2, 512, 128, "mxfp8")
+        for a, b in ((half.k, cache.k), (half.v, cache.v), (half.k_scale, cache.k_scale), (half.v_scale, cache.v_scale)):
+            a[:, :, :hi - lo] = b[:, :, lo:hi]
+        parts.append(tree_attention(q, half, i32([hi - lo - 1])))
+    o, l = merge(torch.stack([p[0].float() for p in parts]), torch.stack([p[1] for p in parts]), torch.float32)
+    ref = oracle.tree_reference(q.double().cpu().numpy(), *vals, [300], None, None, 0, 0, 128 ** -0.5)
+    # the halves' outputs were rounded to bf16 once more on the way
+    assert (np.abs(o.double().cpu().numpy() - ref[0]) <= 3 * 2.0 ** -8 * ref[2] + 2.0 ** -12).all()
+    assert (l - lse).abs().max().item() <= 1e-4
+
+
+def test_bad_sequences_and_parents_are_reported(cuda_lib):
+    q, cache, vals = make(3, 2, 2, 64, 2, [40, 40, 40], "mxfp8", 81, cap=48)
+    ws = tree_workspace(q, cache)
+    out, lse = tree_attention(q, cache, i32([40, -1, 47]), workspace=ws)  # 47 + 2 rows do not fit in 48
+    assert status(ws) == binding.EINVAL
+    ref = oracle.tree_reference(q.double().cpu().numpy(), *vals, [40, 0, 0], None, [2, 0, 0], 0, 0, 1 / 8)
+    check(out, lse, ref, 64)
+    out, lse = tree_attention(q, cache, i32([40, 40, 40]), i32([[-1, 1], [5, 0], [-7, -1]]), workspace=ws)
+    assert status(ws) == binding.EINVAL
+    ref = oracle.tree_reference(q.double().cpu().numpy(), *vals, [40] * 3, [[-1, -1], [-1, 0], [-1, -1]], None, 0, 0, 1 / 8)
+    check(out, lse, ref, 64)
+    tree_attention(q, cache, i32([40, 40, 40]), workspace=ws)
+    assert status(ws) == 0
+    tree_attention(q, cache, i32([40, 40, 40]), counts=i32([2, 3, -1]), workspace=ws)
+    assert status(ws) == binding.EINVAL
+
+
+def test_refusals(cuda_lib):
+    q, cache, _ = make(1, 2, 2, 64, 2, [10], "mxfp8", 91)
+    for bad in (dict(lengths=torch.tensor([10], device="cuda")), dict(parents=i32([[0]])), dict(counts=i32([1, 1]))):
+        a = dict(lengths=i32([10])) | bad
+        with pytest.raises(ValueError):
+            tree_attention(q, cache, **a)
+    for x in (q.float(), q[0], q[..., :32], q.transpose(2, 3).contiguous().transpose(2, 3)):
+        with pytest.raises(ValueError):
+            tree_attention(x, cache, i32([10]))
+    with pytest.raises(RingAttnError) as e:
+        tree_attention(q, cache, i32([10]), workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == binding.EWORKSPACE
+    for kw in (dict(window=-1), dict(sinks=-1), dict(scale=0.0), dict(scale=float("nan"))):
+        with pytest.raises(RingAttnError) as e:
+            tree_attention(q, cache, i32([10]), **kw)
+        assert e.value.code == binding.EINVAL
+    with pytest.raises(RingAttnError):
+        tree_attention(torch.empty(1, 2, 65, 64, dtype=torch.bfloat16, device="cuda"), cache, i32([10]))
+    with pytest.raises(RingAttnError):
+        tree_attention(torch.empty(1, 3, 1, 64, dtype=torch.bfloat16, device="cuda"), cache, i32([10]))
+    with pytest.raises(RingAttnError) as e:
+        flat = torch.empty(1 * 2 * 2 * 64 + 8, dtype=torch.bfloat16, device="cuda")
+        tree_attention(flat[4:260].view(1, 2, 2, 64), cache, i32([10]))
+    assert e.value.code == binding.EALIGN
+
+
+def test_graph_replay_follows_the_lengths(cuda_lib):
+    """One captured call replayed as the sequences grow; lengths, counts and parents are read on the device."""
+    B, T = 2, 3
+    q, cache, vals = make(B, 4, 2, 128, T, [3000, 2000], "mxfp4", 95, cap=4096)
+    lengths, par = i32([1, 1]), i32(random_tree(B, T, 1))
+    ws = tree_workspace(q, cache)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        tree_attention(q, cache, lengths, par, workspace=ws)
+        with torch.cuda.graph(graph, stream=s):
+            out, lse = tree_attention(q, cache, lengths, par, workspace=ws)
+    for n, seed in (([0, 17], 2), ([3000, 2000], 3)):
+        tree = random_tree(B, T, seed)
+        lengths.copy_(i32(n))
+        par.copy_(i32(tree))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = oracle.tree_reference(q.double().cpu().numpy(), *vals, n, tree, None, 0, 0, 128 ** -0.5)
+        check(out, lse, ref, 128, str(n))
