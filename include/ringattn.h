@@ -334,6 +334,31 @@ int ring_attn_tree(const void* q, const int64_t* q_strides, const void* k_cache,
                    int window, int sinks, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Causal attention with a sliding window and sinks: query token t sees the keys of the last
+ * `window` tokens up to its own (u > t - window, u <= t) and of the first `sinks` tokens
+ * (u < sinks, u <= t), so every row sees at least its own key.
+ *   q, out [B, Hq, S, D], k, v [B, Hkv, S, D] bf16; lse [B, Hq, S] fp32 (natural log)
+ *   window >= 1, sinks >= 0 (either may exceed S); any S >= 1; D in {64, 128}
+ *   workspace >= 256 bytes: the status word
+ * Values must be finite. Same argument, workspace and watchdog rules as ring_attn_fwd.
+ */
+int ring_attn_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
+                         int B, int Hq, int Hkv, int64_t S, int D, int64_t window, int64_t sinks, float scale,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of ring_attn_window_fwd's out against dout, from its out and lse (the formulas
+ * of ring_attn_bwd on this mask): dq [B, Hq, S, D], dk, dv [B, Hkv, S, D] bf16. No atomics:
+ * the same call gives the same bits. workspace >= ring_attn_window_bwd_workspace_bytes()
+ * (0 for invalid arguments); one call at a time may use it. Outputs must not alias inputs.
+ */
+size_t ring_attn_window_bwd_workspace_bytes(int B, int Hq, int Hkv, int64_t S, int D, int64_t window, int64_t sinks);
+int ring_attn_window_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                         const void* dout, void* dq, void* dk, void* dv,
+                         int B, int Hq, int Hkv, int64_t S, int D, int64_t window, int64_t sinks, float scale,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronise `stream` and read the status word at the start of `workspace`
  * (written by the last compute call that used it): 0, or RING_ATTN_ETIMEOUT.
  * Returns RING_ATTN_ECUDA if the stream reports an error.
@@ -421,6 +446,16 @@ int64_t ring_attn_debug_unit_walk(int B, int Hq, int Hkv, int64_t S, int P, int 
  */
 int ring_attn_debug_schedule_info(int B, int Hq, int Hkv, int64_t S, int D, int P,
                                   int causal, int layout, int64_t* info);
+
+/*
+ * Host only, no GPU. Walks the schedule and per-element masks of the window kernels and
+ * adds 1 to counts[t*S + u] for every (query token t, key token u) pair they let in: pass 0
+ * the forward, pass 1 the dK/dV pass (batch 0's first kv head: Hq/Hkv times each pair),
+ * pass 2 the dQ pass. counts: host S*S int32 zeroed by the caller, S <= 4096. Returns the
+ * number of tile visits, or a negative error code.
+ */
+int64_t ring_attn_debug_window_visit_counts(int Hq, int Hkv, int64_t S, int D, int64_t window, int64_t sinks, int pass,
+                                            int32_t* counts);
 
 /*
  * Device test of the fused kernel's software 2^x (FMA-pipe polynomial used for a

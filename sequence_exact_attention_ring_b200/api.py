@@ -246,6 +246,83 @@ def ring_attention_decode(q1, k, v, P: int, layout="striped", scale: float | Non
     return out, lse
 
 
+def _check_window(q, k, v, window, sinks):
+    _check_qkv(q, k, v)
+    if q.dtype != torch.bfloat16:
+        raise ValueError("window attention takes bfloat16 tensors")
+    if not (q.device == k.device == v.device):
+        raise ValueError("q, k, v must be on one device")
+    if int(window) < 1 or int(sinks) < 0:
+        raise ValueError("window must be >= 1 and sinks >= 0")
+
+
+def _like(t, ref, name, shape, dtype):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != ref.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the inputs' device")
+    return t
+
+
+def _window_scratch(workspace, need, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.device != device:
+        raise ValueError("workspace must be on the inputs' device")
+    return workspace
+
+
+def window_attention(q, k, v, window: int, sinks: int = 0, scale: float | None = None, out=None, lse=None,
+                     workspace=None, stream=None):
+    """Causal attention in which token t sees the last `window` tokens up to itself and the
+    first `sinks` tokens (attention sinks). q [B,Hq,S,D], k/v [B,Hkv,S,D] bf16, D 64 or 128.
+
+    Returns (out [B,Hq,S,D] bf16, lse [B,Hq,S] fp32). Asynchronous on `stream`.
+    """
+    _check_window(q, k, v, window, sinks)
+    B, Hq, S, D = q.shape
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    out = _like(out, q, "out", (B, Hq, S, D), torch.bfloat16)
+    lse = _like(lse, q, "lse", (B, Hq, S), torch.float32)
+    workspace = _window_scratch(workspace, 256, q.device)
+    with torch.cuda.device(q.device):
+        rc = _b.ring_attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq,
+                                     k.shape[1], S, D, int(window), int(sinks), scale, workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _b.check(rc, "ring_attn_window_fwd")
+    return out, lse
+
+
+def window_attention_backward(q, k, v, out, lse, dout, window: int, sinks: int = 0, scale: float | None = None,
+                              workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of window_attention's output against dout, from its out and lse.
+
+    Asynchronous on `stream`.
+    """
+    _check_window(q, k, v, window, sinks)
+    B, Hq, S, D = q.shape
+    for t, name in ((out, "out"), (dout, "dout")):
+        if t.shape != q.shape or t.dtype != q.dtype or t.device != q.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor shaped and typed like q")
+    if lse.shape != (B, Hq, S) or lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [B, Hq, S] tensor")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    if workspace is None:
+        need = _b.ring_attn_window_bwd_workspace_bytes(B, Hq, k.shape[1], S, D, int(window), int(sinks))
+        if need == 0:
+            raise _b.RingAttnError(_b.EINVAL, "ring_attn_window_bwd_workspace_bytes")
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace = _window_scratch(workspace, 0, q.device)
+    with torch.cuda.device(q.device):
+        rc = _b.ring_attn_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                     dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, k.shape[1], S,
+                                     D, int(window), int(sinks), scale, workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _b.check(rc, "ring_attn_window_bwd")
+    return dq, dk, dv
+
+
 def merge(o_parts: torch.Tensor, lse_parts: torch.Tensor, out_dtype=torch.float32, stream=None):
     """Merge normalised partials o_parts [n, ..., D] fp32 / lse_parts [n, ...] -> (out [..., D], lse [...])."""
     if o_parts.dtype != torch.float32 or lse_parts.dtype != torch.float32:

@@ -77,6 +77,12 @@ SIGNATURES = {
     "ring_attn_tree_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_i64, _c_int, _c_int]),
     "ring_attn_tree": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_i64, _c_int,
                                 _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_float, _vp, _c_size, _vp]),
+    "ring_attn_window_fwd": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_i64, _c_int, _c_i64, _c_i64,
+                                      _c_float, _vp, _c_size, _vp]),
+    "ring_attn_window_bwd_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_i64, _c_int, _c_i64, _c_i64]),
+    "ring_attn_window_bwd": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_i64,
+                                      _c_int, _c_i64, _c_i64, _c_float, _vp, _c_size, _vp]),
+    "ring_attn_debug_window_visit_counts": (_c_i64, [_c_int, _c_int, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _vp]),
     "ring_attn_debug_bwd_visit_counts": (_c_i64, [_c_i64, _c_int, _c_int, _c_int, _c_int, _vp]),
     "ring_attn_fwd_noalloc": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_i64, _c_int, _c_int,
                                        _c_int, _c_int, _c_float, _c_int, _vp, ctypes.POINTER(_vp)]),
@@ -238,6 +244,26 @@ def ring_attn_tree(q, q_strides, k_cache, v_cache, k_scale, v_scale, format_, ou
     return load().ring_attn_tree(q, _strides(q_strides), k_cache, v_cache, k_scale, v_scale, format_, out, lse, B, Hq,
                                  Hkv, capacity, D, T, lengths, parents, counts, window, sinks, scale, workspace,
                                  workspace_bytes, stream)
+
+
+def ring_attn_window_fwd(q, k, v, out, lse, B, Hq, Hkv, S, D, window, sinks, scale, workspace, workspace_bytes,
+                         stream) -> int:
+    return load().ring_attn_window_fwd(q, k, v, out, lse, B, Hq, Hkv, S, D, window, sinks, scale, workspace,
+                                       workspace_bytes, stream)
+
+
+def ring_attn_window_bwd_workspace_bytes(B, Hq, Hkv, S, D, window, sinks) -> int:
+    return load().ring_attn_window_bwd_workspace_bytes(B, Hq, Hkv, S, D, window, sinks)
+
+
+def ring_attn_window_bwd(q, k, v, out, lse, dout, dq, dk, dv, B, Hq, Hkv, S, D, window, sinks, scale, workspace,
+                         workspace_bytes, stream) -> int:
+    return load().ring_attn_window_bwd(q, k, v, out, lse, dout, dq, dk, dv, B, Hq, Hkv, S, D, window, sinks, scale,
+                                       workspace, workspace_bytes, stream)
+
+
+def ring_attn_debug_window_visit_counts(Hq, Hkv, S, D, window, sinks, pass_, counts) -> int:
+    return load().ring_attn_debug_window_visit_counts(Hq, Hkv, S, D, window, sinks, pass_, counts)
 
 
 def ring_attn_debug_bwd_visit_counts(S, P, causal, layout, pass_, counts) -> int:

@@ -459,6 +459,70 @@ int ring_attn_tree(const void* q, const int64_t* q_strides, const void* k_cache,
                      watchdog_ns(), static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+int check_window(int B, int Hq, int Hkv, int64_t S, int D, int64_t window, int64_t sinks, WinGeom* g) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || S <= 0 || D <= 0 || Hq % Hkv != 0) return RING_ATTN_EINVAL;
+  if (window < 1 || sinks < 0) return RING_ATTN_EINVAL;
+  if ((int64_t)B * Hq > (1 << 24) || S > ((int64_t)1 << 30)) return RING_ATTN_EINVAL;
+  if (D != 64 && D != 128) return RING_ATTN_EUNSUPPORTED;
+  g->B = B;
+  g->Hq = Hq;
+  g->Hkv = Hkv;
+  g->D = D;
+  g->S = S;
+  g->window = window < S ? window : S;
+  // a window that holds the whole sequence leaves nothing to sinks
+  g->sinks = g->window == S ? 0 : (sinks < S ? sinks : S);
+  return RING_ATTN_OK;
+}
+
+}  // namespace
+
+int ring_attn_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse, int B, int Hq, int Hkv,
+                         int64_t S, int D, int64_t window, int64_t sinks, float scale, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  WinGeom g;
+  int rc = check_window(B, Hq, Hkv, S, D, window, sinks, &g);
+  if (rc) return rc;
+  if (!q || !k || !v || !out || !lse) return RING_ATTN_EINVAL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse)) return RING_ATTN_EALIGN;
+  if (!workspace || workspace_bytes < kWorkspaceHeaderBytes || !aligned16(workspace)) return RING_ATTN_EWORKSPACE;
+  if (!(scale > 0.f) || !isfinite(scale)) return RING_ATTN_EINVAL;
+  if (!device_is_sm100()) return RING_ATTN_EUNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((rc = reset_status(workspace, st))) return rc;
+  return launch_window_fwd(q, k, v, out, lse, g, scale, static_cast<int*>(workspace), watchdog_ns(), st);
+}
+
+size_t ring_attn_window_bwd_workspace_bytes(int B, int Hq, int Hkv, int64_t S, int D, int64_t window, int64_t sinks) {
+  WinGeom g;
+  if (check_window(B, Hq, Hkv, S, D, window, sinks, &g) != RING_ATTN_OK) return 0;
+  return kWorkspaceHeaderBytes + window_bwd_scratch_bytes(g);
+}
+
+int ring_attn_window_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                         const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int64_t S, int D,
+                         int64_t window, int64_t sinks, float scale, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  WinGeom g;
+  int rc = check_window(B, Hq, Hkv, S, D, window, sinks, &g);
+  if (rc) return rc;
+  if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv) return RING_ATTN_EINVAL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse) || !aligned16(dout) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return RING_ATTN_EALIGN;
+  if (!workspace || workspace_bytes < kWorkspaceHeaderBytes + window_bwd_scratch_bytes(g) || !aligned16(workspace))
+    return RING_ATTN_EWORKSPACE;
+  if (!(scale > 0.f) || !isfinite(scale)) return RING_ATTN_EINVAL;
+  if (!device_is_sm100()) return RING_ATTN_EUNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((rc = reset_status(workspace, st))) return rc;
+  float* scratch = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeaderBytes);
+  return launch_window_bwd(q, k, v, out, lse, dout, dq, dk, dv, g, scale, scratch, static_cast<int*>(workspace),
+                           watchdog_ns(), st);
+}
+
 int ring_attn_status(const void* workspace, void* stream) {
   if (!workspace) return RING_ATTN_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -616,6 +680,15 @@ int ring_attn_debug_schedule_info(int B, int Hq, int Hkv, int64_t S, int D, int 
   info[4] = first;
   info[5] = last;
   return RING_ATTN_OK;
+}
+
+int64_t ring_attn_debug_window_visit_counts(int Hq, int Hkv, int64_t S, int D, int64_t window, int64_t sinks, int pass,
+                                            int32_t* counts) {
+  WinGeom g;
+  int rc = check_window(1, Hq, Hkv, S, D, window, sinks, &g);
+  if (rc) return rc;
+  if (!counts || S > 4096 || pass < 0 || pass > 2) return RING_ATTN_EINVAL;
+  return pass == 0 ? window_fwd_visits(g, counts) : window_bwd_visits(g, pass - 1, counts);
 }
 
 int ring_attn_debug_exp2(const float* x, float* y, int64_t n, void* stream) {

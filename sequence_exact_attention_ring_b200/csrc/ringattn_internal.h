@@ -7,6 +7,7 @@
 
 #include "ringattn.h"
 #include "ring_schedule.h"
+#include "window_geom.h"
 
 namespace ringattn {
 
@@ -20,6 +21,10 @@ int encode_shard_map(CUtensorMap* map, const void* base, const RingGeom& g, int 
 // (coordinates from tile_coords), else encode_shard_map.
 int encode_input_map(CUtensorMap* map, const void* base, const RingGeom& g, bool local, int heads, int D,
                      int box_rows);
+
+// TMA map of a [bh, S, D] bf16 tensor with the same coordinates (column, row, 0, bh) and box
+// as a one-shard encode_shard_map; rows past S read as zeros.
+int encode_rows_map(CUtensorMap* map, const void* base, int64_t bh, int64_t S, int D, int box_rows);
 
 // Status word layout at the start of the caller's workspace.
 constexpr size_t kWorkspaceHeaderBytes = 256;
@@ -121,6 +126,19 @@ size_t tree_workspace_bytes(const CacheView& c, int Hq, int T);
 int launch_tree(const CacheView& c, const void* q, const int64_t* qs, void* out, float* lse, const int32_t* lengths,
                 const int32_t* parents, const int32_t* counts, int Hq, int T, int window, int sinks, float scale,
                 void* workspace, uint64_t watchdog_ns, cudaStream_t stream);
+
+// Causal attention with a sliding window and sinks (bf16): forward, and gradients with
+// `scratch` of window_bwd_scratch_bytes(g).
+int launch_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse, const WinGeom& g,
+                      float scale, int* status, uint64_t watchdog_ns, cudaStream_t stream);
+size_t window_bwd_scratch_bytes(const WinGeom& g);
+int launch_window_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
+                      void* dq, void* dk, void* dv, const WinGeom& g, float scale, float* scratch, int* status,
+                      uint64_t watchdog_ns, cudaStream_t stream);
+
+// Host walks of their schedules and masks (see ring_attn_debug_window_visit_counts).
+int64_t window_fwd_visits(const WinGeom& g, int32_t* counts);
+int64_t window_bwd_visits(const WinGeom& g, int pass, int32_t* counts);
 
 int launch_merge(const float* o_parts, const float* lse_parts, int n_parts, int64_t rows, int D, void* out,
                  float* lse_out, int out_dtype, cudaStream_t stream);

@@ -66,4 +66,16 @@ int encode_input_map(CUtensorMap* map, const void* base, const RingGeom& g, bool
   return encode_shard_map(map, base, one, heads, D, box_rows);
 }
 
+int encode_rows_map(CUtensorMap* map, const void* base, int64_t bh, int64_t S, int D, int box_rows) {
+  RingGeom g;
+  g.B = 1;
+  g.Hq = g.Hkv = (int)bh;
+  g.S = g.Sq = S;
+  g.D = D;
+  g.P = 1;
+  g.causal = 1;
+  g.layout = kContiguous;
+  return encode_shard_map(map, base, g, (int)bh, D, box_rows);
+}
+
 }  // namespace ringattn
