@@ -4,25 +4,37 @@
 // Mathematics: online softmax over the visible keys in base 2, m = reference maximum,
 // p = 2^(s scale log2 e - m), l = sum p, O = sum p v, result O / l and m + log2 l.
 //
-// What bounds it: reading the cache once. A group of 16 query rows is one m16n8k16 tile,
-// and every warp works alone on 16 keys at a time: it keeps its own ring of cache rows in
-// shared memory (16-byte asynchronous copies, no block barrier in the loop), converts
-// codes to bf16 in registers straight into the operand fragments, and holds the group's
+// What bounds it: reading the cache once; then the instructions that turn codes into
+// operands. Every warp works alone on kStep keys at a time: it keeps its own ring of cache
+// rows in shared memory (16-byte asynchronous copies, no block barrier in the loop),
+// converts codes in registers straight into the operand fragments, and holds the group's
 // queries, running state and output in registers. Nothing that was dequantised is written
-// anywhere. The tensor work is small here (one row tile), which is why this form uses the
-// warp-level matrix instructions: their operands come from registers, whereas tcgen05
-// reads them from shared memory, where the dequantised tile would have to be written and
-// read again (1536 of 1460 clocks that HBM needs for 128 mxfp8 keys).
+// anywhere. The tensor work is small here, which is why this form uses the warp-level matrix
+// instructions: their operands come from registers, whereas tcgen05 reads them from shared
+// memory, where the dequantised tile would have to be written and read again.
 //
-// Codes to bf16 without a conversion instruction: the code's sign goes to the sign bit,
-// its exponent and mantissa to the low exponent and high mantissa bits. That bf16 value is
-// the code's value times 2^-120 (e4m3) or 2^-126 (e2m1), subnormal codes included, and one
-// exact multiplication by a power of two brings in the block's scale. To keep that factor
-// inside bf16's range for every scale up to 2^63, K and V are held 2^62 too small and Q and
-// P 2^62 too large; the products are those of the true values. A block whose scale is
-// larger reads as NaN. Which head dimension or key meets which k index of a matrix
-// instruction is free as long as both operands agree, so the pairs are those that a word
-// of codes yields by shifts: (0,2),(1,3) of four 8-bit codes, (i, i+4) of eight 4-bit ones.
+// The products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so that keys and head
+// dimensions fill the 16 rows of an m16n8k16 tile and 8 query rows its columns: a decode
+// step's 1 to 8 rows per kv head then cost half the instructions and registers of a 16-row
+// tile. P^T changes sides between the products by one 8x8 transpose per 8 keys.
+//
+// Microscaled codes become fp16 operands: two codes per conversion instruction, one packed
+// multiplication by the block's scale. fp16 holds every code exactly; its small exponent
+// range is met by references that are powers of two, so nothing but the far end of the
+// range is ever rounded:
+//   * a step's K (and V) scales are taken relative to the largest one in the step, R;
+//   * a query row is scaled so that its largest element lies in [2^14, 2^15);
+//   * the weights p = 2^(s - m) <= 2^2 enter as p 2^(R - E + 13), where E is the largest R of
+//     V so far (O is rescaled in the rare step that raises it) and R >= E - 3: fp16 then
+//     rounds p to 11 bits down to 2^-24, and below that by at most 2^-35 (half its smallest
+//     step, 2^-25, over 2^10), 2^-15 in all for the weights of 2^20 keys.
+// A step that does not fit (scales more than 2^15 apart, R more than 2^3 below E, a block
+// that is not finite) takes the same products in bf16, whose range they always fit: the
+// code's sign, exponent and mantissa bits are moved to bf16's, which gives its value times
+// 2^-120 (e4m3) or 2^-126 (e2m1), and the multiplication by the scale makes up for that.
+//
+// Which head dimension or key meets which k index of a matrix instruction is free as long
+// as both operands agree, so lanes load 16 contiguous bytes and use them in memory order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -36,28 +48,38 @@ namespace tree {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 16;    // query rows per group
-constexpr int kStep = 16;    // keys per warp and step
-constexpr float kLift = 62.f;            // log2 of the factor between held and true K, V (see above)
-constexpr float kRescale = 8.f;          // the reference maximum moves when a score passes it by this
+constexpr int kLiftP = 13;   // log2 of the factor that p carries into fp16 (see above)
+constexpr int kSpread = 15;  // scales of a step may lie 2^kSpread apart in the fp16 form
+constexpr int kBelow = 3;    // and R this far below E
+// The reference maximum moves when a score passes it by this (base 2): the room that p needs
+// at the top of fp16's range, and more than bf16 has use for.
+template <int FMT>
+__host__ __device__ constexpr float rescale_log2() {
+  return FMT == RING_ATTN_CACHE_BF16 ? 8.f : 2.f;
+}
 
 template <int FMT, int D>
 struct Fmt {
   static constexpr int kRowBytes = cache_row_bytes<FMT>(D);
   static constexpr int kChunks = kRowBytes / 16;             // 16-byte chunks per row
   static constexpr bool kMx = FMT != RING_ATTN_CACHE_BF16;
+  static constexpr int kStep = kMx || D == 64 ? 32 : 16;     // keys per warp and step
+  static constexpr int kSubs = kStep / 16;
   static constexpr int kScaleRow = kMx ? D / kMxBlock : 0;   // scale bytes per row
   static constexpr int kTileBytes = kStep * kRowBytes;       // K or V of one step
-  static constexpr int kScaleBytes = kStep * kScaleRow;
-  static constexpr int kStageBytes = 2 * kTileBytes + (kMx ? 128 : 0);
-  static constexpr int kStages = FMT == RING_ATTN_CACHE_BF16 ? (D == 128 ? 3 : 4) : (FMT == RING_ATTN_CACHE_MXFP8 ? 4 : 6);
-  static constexpr int kMerge = kWarps * kRows * (D + 4) * 4;  // end of unit: O of every warp
-  static constexpr int kRing = kWarps * kStages * kStageBytes;
-  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kScaleBytes = kStep * kScaleRow;      // K or V scales of one step
+  static constexpr int kStageBytes = 2 * kTileBytes + 2 * kScaleBytes;
+  // ring stages: two steps ahead of 12 warps per SM, as far as shared memory goes
+  static constexpr int kStagesFit = (232448 / 3 - 4096) / (kWarps * kStageBytes);
+  static constexpr int kStages = kStagesFit < 4 ? kStagesFit : 4;
+  static_assert(kStages >= 2, "a step is loaded while another is worked on");
   static constexpr int kKSteps = D / 16;                     // k16 steps of the score product
-  // resident CTAs per SM: what registers allow (168 or 128 a thread), less where the rings fill shared memory
-  static constexpr int kFit = 232448 / (kSmem + 4096);
-  static constexpr int kPerSm = kFit < (D == 128 ? 3 : 4) ? kFit : (D == 128 ? 3 : 4);
+  // resident CTAs: 168 registers a thread, or 255 for the tile that needs them
+  static constexpr int per_sm(int nt) { return D == 128 && nt == 2 ? 2 : 3; }
+  static constexpr int smem(int rows) {
+    const int ring = kWarps * kStages * kStageBytes, merge = kWarps * rows * (D + 4) * 4;
+    return ring > merge ? ring : merge;
+  }
 };
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool live) {
@@ -73,11 +95,18 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+template <bool kHalf>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  if constexpr (kHalf)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -85,26 +114,148 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 2^e, 0 below 2^-126 (e <= 127).
+__device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(e + 127) << 23); }
+// An fp16 pair as bf16 (exact for what a query holds, see the head of the file).
+__device__ __forceinline__ uint32_t bf16_of_f16(uint32_t a) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  return pack_bf16x2(f.x, f.y);
+}
+// Two e4m3 codes (the low or high half of a word) to fp16.
+template <int H>
+__device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t w) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)(H ? w >> 16 : w)));
+  return d;
+}
+// Two e2m1 codes (byte I of a word) to fp16.
+template <int I>
+__device__ __forceinline__ uint32_t e2m1_f16x2(uint32_t w) {
+  uint32_t d;
+  if constexpr (I == 0)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(d) : "r"(w));
+  else if constexpr (I == 1)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(d) : "r"(w));
+  else if constexpr (I == 2)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(d) : "r"(w));
+  else
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(d) : "r"(w));
+  return d;
+}
 
-// bf16 (exponent field shifted, see the head of the file) pairs from a word of codes:
-// e4m3 bytes 0 and 2 (Odd = false) or 1 and 3.
+// bf16 with the code's bits in place (times 2^-120 or 2^-126, see the head of the file):
+// e4m3 bytes 0 and 2 (Odd = false) or 1 and 3; e2m1 nibbles I and I + 4.
 template <bool Odd>
 __device__ __forceinline__ uint32_t e4m3_raw(uint32_t w) {
   if (!Odd) w <<= 8;
   return ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
 }
-// e2m1 nibbles I and I + 4.
 template <int I>
 __device__ __forceinline__ uint32_t e2m1_raw(uint32_t w) {
   const uint32_t x = w << (12 - 4 * I);
   return ((x >> 6) & 0x01c001c0u) | (x & 0x80008000u);
 }
 
-// 2^(byte - 127 + lift of the raw form - 62) as bf16 bits; NaN above a scale of 2^63.
+// Pairs of adjacent elements of a word of codes, times the factors f: fp16 or bf16.
+template <int FMT, bool kHalf>
+__device__ __forceinline__ void word_pairs(uint32_t w, uint32_t f, uint32_t* out) {
+  if constexpr (FMT == RING_ATTN_CACHE_MXFP8) {
+    if constexpr (kHalf) {
+      out[0] = mul_f16x2(e4m3_f16x2<0>(w), f);
+      out[1] = mul_f16x2(e4m3_f16x2<1>(w), f);
+    } else {
+      const uint32_t e = mul_bf16x2(e4m3_raw<false>(w), f), o = mul_bf16x2(e4m3_raw<true>(w), f);
+      out[0] = __byte_perm(e, o, 0x5410);
+      out[1] = __byte_perm(e, o, 0x7632);
+    }
+  } else {
+    if constexpr (kHalf) {
+      out[0] = mul_f16x2(e2m1_f16x2<0>(w), f);
+      out[1] = mul_f16x2(e2m1_f16x2<1>(w), f);
+      out[2] = mul_f16x2(e2m1_f16x2<2>(w), f);
+      out[3] = mul_f16x2(e2m1_f16x2<3>(w), f);
+    } else {
+      const uint32_t r0 = mul_bf16x2(e2m1_raw<0>(w), f), r1 = mul_bf16x2(e2m1_raw<1>(w), f);
+      const uint32_t r2 = mul_bf16x2(e2m1_raw<2>(w), f), r3 = mul_bf16x2(e2m1_raw<3>(w), f);
+      out[0] = __byte_perm(r0, r1, 0x5410);
+      out[1] = __byte_perm(r2, r3, 0x5410);
+      out[2] = __byte_perm(r0, r1, 0x7632);
+      out[3] = __byte_perm(r2, r3, 0x7632);
+    }
+  }
+}
+
+// Pairs (key a, key b) of every element of two words of codes, times the factors f (low
+// half a's, high half b's), in element order.
+template <int FMT, bool kHalf>
+__device__ __forceinline__ void key_pairs(uint32_t a, uint32_t b, uint32_t f, uint32_t* out) {
+  if constexpr (FMT == RING_ATTN_CACHE_BF16) {
+    out[0] = __byte_perm(a, b, 0x5410);
+    out[1] = __byte_perm(a, b, 0x7632);
+  } else if constexpr (FMT == RING_ATTN_CACHE_MXFP8) {
+    if constexpr (kHalf) {
+      const uint32_t x = __byte_perm(a, b, 0x5140), y = __byte_perm(a, b, 0x7362);
+      out[0] = mul_f16x2(e4m3_f16x2<0>(x), f);
+      out[1] = mul_f16x2(e4m3_f16x2<1>(x), f);
+      out[2] = mul_f16x2(e4m3_f16x2<0>(y), f);
+      out[3] = mul_f16x2(e4m3_f16x2<1>(y), f);
+    } else {
+      const uint32_t x = __byte_perm(a, b, 0x5410), y = __byte_perm(a, b, 0x7632);
+      out[0] = mul_bf16x2(e4m3_raw<false>(x), f);
+      out[1] = mul_bf16x2(e4m3_raw<true>(x), f);
+      out[2] = mul_bf16x2(e4m3_raw<false>(y), f);
+      out[3] = mul_bf16x2(e4m3_raw<true>(y), f);
+    }
+  } else {
+    if constexpr (kHalf) {
+      const uint32_t x = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);  // elements 0, 2, 4, 6
+      const uint32_t y = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);  // elements 1, 3, 5, 7
+      out[0] = mul_f16x2(e2m1_f16x2<0>(x), f);
+      out[1] = mul_f16x2(e2m1_f16x2<0>(y), f);
+      out[2] = mul_f16x2(e2m1_f16x2<1>(x), f);
+      out[3] = mul_f16x2(e2m1_f16x2<1>(y), f);
+      out[4] = mul_f16x2(e2m1_f16x2<2>(x), f);
+      out[5] = mul_f16x2(e2m1_f16x2<2>(y), f);
+      out[6] = mul_f16x2(e2m1_f16x2<3>(x), f);
+      out[7] = mul_f16x2(e2m1_f16x2<3>(y), f);
+    } else {
+      const uint32_t x = __byte_perm(a, b, 0x5410), y = __byte_perm(a, b, 0x7632);
+      out[0] = mul_bf16x2(e2m1_raw<0>(x), f);
+      out[1] = mul_bf16x2(e2m1_raw<1>(x), f);
+      out[2] = mul_bf16x2(e2m1_raw<2>(x), f);
+      out[3] = mul_bf16x2(e2m1_raw<3>(x), f);
+      out[4] = mul_bf16x2(e2m1_raw<0>(y), f);
+      out[5] = mul_bf16x2(e2m1_raw<1>(y), f);
+      out[6] = mul_bf16x2(e2m1_raw<2>(y), f);
+      out[7] = mul_bf16x2(e2m1_raw<3>(y), f);
+    }
+  }
+}
+
+// log2 of the factor that operands carry beside the scale: keeps the smallest codes well
+// inside fp16 and the bf16 form's factor within 2^127.
 template <int FMT>
-__device__ __forceinline__ uint32_t raw_factor(uint32_t byte) {
-  constexpr uint32_t up = FMT == RING_ATTN_CACHE_MXFP8 ? 58u : 64u;  // 120 - 62, 126 - 62
-  return byte > 190u ? 0x7fc0u : (byte + up) << 7;
+__host__ __device__ constexpr int lift_code() {
+  return FMT == RING_ATTN_CACHE_MXFP8 ? 7 : 1;
+}
+
+// 2^(byte - ref + lift) for an fp16 pair's half, or the same times 2^120 or 2^126 for the
+// bf16 form (NaN for a block that is not finite, 0 far below the reference).
+template <int FMT, bool kHalf>
+__device__ __forceinline__ uint32_t code_factor(int byte, int ref) {
+  if (kHalf) return (uint32_t)(byte - ref + lift_code<FMT>() + 15) << 10;
+  const int e = byte - ref + lift_code<FMT>() + (FMT == RING_ATTN_CACHE_MXFP8 ? 120 : 126) + 127;
+  return byte == 255 ? 0x7fc0u : (e <= 0 ? 0u : (uint32_t)e << 7);
 }
 
 // Chunk positions inside a row of the ring (16-byte units) that keep the fragment loads
@@ -114,14 +265,14 @@ __device__ __forceinline__ int k_pos(int row, int ch) {
   return NC >= 8 ? ch ^ ((row & 1) << 2) : ch;
 }
 template <int NC>
-__device__ __forceinline__ int v_slot(int row) {  // row's place among the 16
-  return NC <= 4 ? (row >> 1) | ((row & 1) << 3) : row;
+__device__ __forceinline__ int v_slot(int row) {  // row's place in the step (16 rows stay together)
+  return NC <= 4 ? (row & 16) | (row >> 1 & 7) | ((row & 1) << 3) : row;
 }
 template <int NC>
 __device__ __forceinline__ int v_pos(int row, int ch) {
   if (NC == 16) return ch ^ (((row >> 1) & 1) | (row & 4));
   if (NC == 8) return ch ^ (row & 6);
-  if (NC == 4) return ch ^ (((v_slot<NC>(row) >> 1) & 1) << 1);
+  if (NC == 4) return ch ^ ((row >> 2 & 1) << 1);
   return ch;
 }
 
@@ -130,111 +281,187 @@ __device__ __forceinline__ int v_pos(int row, int ch) {
 template <int FMT, int D>
 __device__ __forceinline__ int score_dim(int s, int c, int h, int e) {
   if (FMT == RING_ATTN_CACHE_BF16) return (4 * (s / 2) + c) * 8 + (s % 2) * 4 + h * 2 + e;
-  if (FMT == RING_ATTN_CACHE_MXFP8) return (c + 4 * (s / 4)) * 16 + (s % 4) * 4 + h + 2 * e;
-  return c * (D / 4) + (s / 2) * 8 + (s % 2) * 2 + h + 4 * e;
+  if (FMT == RING_ATTN_CACHE_MXFP8) return (c + 4 * (s / 4)) * 16 + (s % 4) * 4 + h * 2 + e;
+  return c * (D / 4) + s * 4 + h * 2 + e;
 }
 
-template <int FMT, int D>
+// 8x8 transpose of 16-bit elements held two per lane (lane 4 r + c: row r, columns 2c, 2c+1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+template <int FMT, int D, int NT>
 struct Warp {
   using F = Fmt<FMT, D>;
 
-  // Copies of step `i` into ring stage `st` (one commit group, empty when i is out of range).
-  static __device__ __forceinline__ void load(const Params& p, const Keys& ks, int64_t head_row, int i, bool in,
-                                              uint8_t* st) {
+  // Copies of the step whose first key is kb into ring stage `st`. The step's rows are
+  // contiguous: lane l copies bytes 16 l + 512 x.
+  static __device__ __forceinline__ void load(const Params& p, const Keys& ks, int64_t head_row, int kb, uint8_t* st) {
     const int lane = threadIdx.x % 32;
-    if (in) {
-      const int kb = step_key(p, ks, i);
-      const uint8_t* k = static_cast<const uint8_t*>(p.c.k) + (head_row + kb) * F::kRowBytes;
-      const uint8_t* v = static_cast<const uint8_t*>(p.c.v) + (head_row + kb) * F::kRowBytes;
-      constexpr int kCopies = kStep * F::kChunks;
+    const int64_t first = head_row + kb;
+    const uint8_t* k = static_cast<const uint8_t*>(p.c.k) + first * F::kRowBytes + lane * 16;
+    const uint8_t* v = static_cast<const uint8_t*>(p.c.v) + first * F::kRowBytes + lane * 16;
+    constexpr int kCopies = F::kStep * F::kChunks;
+    const bool all = whole_live(p, ks, kb);
 #pragma unroll
-      for (int e0 = 0; e0 < kCopies; e0 += 32) {
-        const int e = e0 + lane;
-        const int row = e / F::kChunks, ch = e % F::kChunks;
-        // a dead row's copy is a zero fill that reads nothing
-        const bool live = key_live(p, ks, kb + row);
-        const int64_t off = live ? (int64_t)row * F::kRowBytes + ch * 16 : 0;
-        cp_async16(st + row * F::kRowBytes + k_pos<F::kChunks>(row, ch) * 16, k + off, live);
-        cp_async16(st + F::kTileBytes + v_slot<F::kChunks>(row) * F::kRowBytes + v_pos<F::kChunks>(row, ch) * 16,
-                   v + off, live);
-      }
-      if (F::kMx) {
-        // the step's scale bytes are contiguous: capacity and kb are multiples of 16 rows
-        constexpr int kWords = F::kScaleBytes / 4;
-        if (lane < kWords)
-          cp_async4(st + 2 * F::kTileBytes + lane * 4,
-                    static_cast<const uint8_t*>(p.c.k_scale) + (head_row + kb) * F::kScaleRow + lane * 4);
-        else if (lane >= 16 && lane < 16 + kWords)
-          cp_async4(st + 2 * F::kTileBytes + 64 + (lane - 16) * 4,
-                    static_cast<const uint8_t*>(p.c.v_scale) + (head_row + kb) * F::kScaleRow + (lane - 16) * 4);
+    for (int e0 = 0; e0 < kCopies; e0 += 32) {
+      const int e = e0 + lane;
+      const int row = e / F::kChunks, ch = e % F::kChunks;
+      // a dead row's copy is a zero fill that reads nothing
+      const bool live = all || key_live(p, ks, kb + row);
+      const int off = live ? e0 * 16 : -lane * 16;
+      cp_async16(st + row * F::kRowBytes + k_pos<F::kChunks>(row, ch) * 16, k + off, live);
+      cp_async16(st + F::kTileBytes + v_slot<F::kChunks>(row) * F::kRowBytes + v_pos<F::kChunks>(row, ch) * 16,
+                 v + off, live);
+    }
+    if (F::kMx) {
+      // scale bytes of 16 rows that start inside the cache lie inside it (capacity and kb are
+      // multiples of 16); the second 16 may lie past its end
+      constexpr int kWords = F::kScaleBytes / 4;  // 32 or 16 per tensor
+      const bool in = lane < kWords / 2 || kb + 16 < p.c.capacity;
+      if (lane < kWords && in) {
+        cp_async4(st + 2 * F::kTileBytes + lane * 4,
+                  static_cast<const uint8_t*>(p.c.k_scale) + first * F::kScaleRow + lane * 4);
+        cp_async4(st + 2 * F::kTileBytes + F::kScaleBytes + lane * 4,
+                  static_cast<const uint8_t*>(p.c.v_scale) + first * F::kScaleRow + lane * 4);
       }
     }
-    cp_commit();
   }
 
-  // Scale byte j of cache row `row` of the step (sc: the step's K or V scale bytes).
-  static __device__ __forceinline__ uint32_t scale_byte(const uint8_t* sc, int row, int j) {
-    return sc[row * F::kScaleRow + j];
+  // All rows of the step that starts at kb can be seen by some query row.
+  static __device__ __forceinline__ bool whole_live(const Params& p, const Keys& ks, int kb) {
+    return kb + F::kStep <= ks.n + ks.cnt &&
+           (p.window <= 0 || kb + F::kStep <= p.sinks || kb > ks.n - p.window);
   }
 
-  // Scores of 16 keys: s[t] the m16n8 tile of keys 8t .. 8t+7.
-  static __device__ __forceinline__ void scores(const uint8_t* st, const uint32_t (&q)[F::kKSteps][4],
-                                                float (&s)[2][4], const bool (&key_ok)[2]) {
-    const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
+  // The largest and smallest scale bytes of the step's live K rows (ref[0], low[0]) and V rows
+  // (ref[1], low[1]).
+  static __device__ __forceinline__ void scale_range(const uint8_t* st, uint32_t live_rows, int (&ref)[2],
+                                                     int (&low)[2]) {
+    const int lane = threadIdx.x % 32;
+    const bool mine = F::kStep == 32 ? (live_rows >> lane & 1) : (lane < 16 && (live_rows >> lane & 1));
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int row = 8 * t + g;
-      const uint8_t* kr = st + row * F::kRowBytes;
-      const uint8_t* sc = st + 2 * F::kTileBytes;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-      if constexpr (FMT == RING_ATTN_CACHE_BF16) {
-#pragma unroll
-        for (int i = 0; i < F::kKSteps / 2; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(kr + k_pos<F::kChunks>(row, 4 * i + c) * 16);
-          mma16816(s[t], q[2 * i], w.x, w.y);
-          mma16816(s[t], q[2 * i + 1], w.z, w.w);
-        }
-      } else if constexpr (FMT == RING_ATTN_CACHE_MXFP8) {
-#pragma unroll
-        for (int i = 0; i < F::kKSteps / 4; ++i) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(kr + k_pos<F::kChunks>(row, c + 4 * i) * 16);
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-          const uint32_t f = key_ok[t] ? raw_factor<FMT>(scale_byte(sc, row, (c + 4 * i) / 2)) * 0x10001u : 0u;
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            mma16816(s[t], q[4 * i + x], mul_bf16x2(e4m3_raw<false>(w[x]), f), mul_bf16x2(e4m3_raw<true>(w[x]), f));
-        }
-      } else {
-        constexpr int kWords = D / 32;  // words of 8 codes per lane
-        uint32_t w[kWords];
-        if constexpr (D == 128) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(kr + c * 16);
-          w[0] = w4.x; w[1] = w4.y; w[2] = w4.z; w[3] = w4.w;
+    for (int i = 0; i < 2; ++i) {
+      const uint8_t* sc = st + 2 * F::kTileBytes + i * F::kScaleBytes;
+      uint32_t hi = 0, lo = 255;
+      if (mine) {
+        if (F::kScaleRow == 4) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
+          const uint32_t a = w & 0x00ff00ffu, b = w >> 8 & 0x00ff00ffu;
+          const uint32_t mx = __vmaxu2(a, b), mn = __vminu2(a, b);
+          hi = max(mx & 0xffffu, mx >> 16);
+          lo = min(mn & 0xffffu, mn >> 16);
         } else {
-          const uint2 w2 = *reinterpret_cast<const uint2*>(kr + c * 8);
-          w[0] = w2.x; w[1] = w2.y;
+          const uint32_t w = *reinterpret_cast<const uint16_t*>(sc + lane * 2);
+          hi = max(w & 255u, w >> 8);
+          lo = min(w & 255u, w >> 8);
         }
-        const uint32_t f = key_ok[t] ? raw_factor<FMT>(scale_byte(sc, row, c * (D / 4) / kMxBlock)) * 0x10001u : 0u;
+      }
+      ref[i] = (int)__reduce_max_sync(0xffffffffu, hi);
+      low[i] = (int)__reduce_min_sync(0xffffffffu, lo);
+    }
+  }
+
+  // d += a b with the query fragment in fp16 and a in fp16 or bf16.
+  template <bool kHalf>
+  static __device__ __forceinline__ void product(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&q)[2]) {
+    if constexpr (kHalf || !F::kMx)
+      mma16816<kHalf>(d, a, q[0], q[1]);
+    else
+      mma16816<false>(d, a, bf16_of_f16(q[0]), bf16_of_f16(q[1]));
+  }
+
+  // Scores of 16 keys (16 sub .. 16 sub + 15 of the step): s[x] the m16n8 tile of query rows
+  // 8x .. 8x+7. live: bits of the rows that hold data (a dead row's codes are zeros, its scale
+  // bytes anything).
+  template <bool kHalf>
+  static __device__ __forceinline__ void scores(const uint8_t* st, int sub, const uint32_t (&q)[NT][F::kKSteps][2],
+                                                float (&s)[NT][4], uint32_t live, int ref) {
+    const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
+    const int row0 = 16 * sub + g, row1 = row0 + 8;
+    const uint8_t* k0 = st + row0 * F::kRowBytes;
+    const uint8_t* k1 = st + row1 * F::kRowBytes;
+    const uint8_t* sc = st + 2 * F::kTileBytes;
 #pragma unroll
-        for (int x = 0; x < kWords; ++x) {
-          mma16816(s[t], q[2 * x], mul_bf16x2(e2m1_raw<0>(w[x]), f), mul_bf16x2(e2m1_raw<1>(w[x]), f));
-          mma16816(s[t], q[2 * x + 1], mul_bf16x2(e2m1_raw<2>(w[x]), f), mul_bf16x2(e2m1_raw<3>(w[x]), f));
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
+    auto factor = [&](int row, int blk) {
+      const int byte = live >> row & 1 ? sc[row * F::kScaleRow + blk] : ref;
+      return code_factor<FMT, kHalf>(byte, ref) * 0x10001u;
+    };
+    if constexpr (FMT == RING_ATTN_CACHE_BF16) {
+#pragma unroll
+      for (int i = 0; i < F::kKSteps / 2; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4*>(k0 + k_pos<F::kChunks>(row0, 4 * i + c) * 16);
+        const uint4 z = *reinterpret_cast<const uint4*>(k1 + k_pos<F::kChunks>(row1, 4 * i + c) * 16);
+        const uint32_t a[4] = {w.x, z.x, w.y, z.y}, b[4] = {w.z, z.z, w.w, z.w};
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          product<false>(s[x], a, q[x][2 * i]);
+          product<false>(s[x], b, q[x][2 * i + 1]);
+        }
+      }
+    } else if constexpr (FMT == RING_ATTN_CACHE_MXFP8) {
+#pragma unroll
+      for (int i = 0; i < F::kKSteps / 4; ++i) {
+        const uint4 w4 = *reinterpret_cast<const uint4*>(k0 + k_pos<F::kChunks>(row0, c + 4 * i) * 16);
+        const uint4 z4 = *reinterpret_cast<const uint4*>(k1 + k_pos<F::kChunks>(row1, c + 4 * i) * 16);
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w}, z[4] = {z4.x, z4.y, z4.z, z4.w};
+        const uint32_t f0 = factor(row0, (c + 4 * i) / 2), f1 = factor(row1, (c + 4 * i) / 2);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t b0[2], b1[2];
+          word_pairs<FMT, kHalf>(w[y], f0, b0);
+          word_pairs<FMT, kHalf>(z[y], f1, b1);
+          const uint32_t a[4] = {b0[0], b1[0], b0[1], b1[1]};
+#pragma unroll
+          for (int x = 0; x < NT; ++x) product<kHalf>(s[x], a, q[x][4 * i + y]);
+        }
+      }
+    } else {
+      constexpr int kWords = D / 32;  // words of 8 codes per lane and row
+      uint32_t w[kWords], z[kWords];
+      if constexpr (D == 128) {
+        const uint4 w4 = *reinterpret_cast<const uint4*>(k0 + c * 16), z4 = *reinterpret_cast<const uint4*>(k1 + c * 16);
+        w[0] = w4.x; w[1] = w4.y; w[2] = w4.z; w[3] = w4.w;
+        z[0] = z4.x; z[1] = z4.y; z[2] = z4.z; z[3] = z4.w;
+      } else {
+        const uint2 w2 = *reinterpret_cast<const uint2*>(k0 + c * 8), z2 = *reinterpret_cast<const uint2*>(k1 + c * 8);
+        w[0] = w2.x; w[1] = w2.y;
+        z[0] = z2.x; z[1] = z2.y;
+      }
+      const uint32_t f0 = factor(row0, c * (D / 4) / kMxBlock), f1 = factor(row1, c * (D / 4) / kMxBlock);
+#pragma unroll
+      for (int y = 0; y < kWords; ++y) {
+        uint32_t b0[4], b1[4];
+        word_pairs<FMT, kHalf>(w[y], f0, b0);
+        word_pairs<FMT, kHalf>(z[y], f1, b1);
+        const uint32_t a[4] = {b0[0], b1[0], b0[1], b1[1]}, b[4] = {b0[2], b1[2], b0[3], b1[3]};
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          product<kHalf>(s[x], a, q[x][2 * y]);
+          product<kHalf>(s[x], b, q[x][2 * y + 1]);
         }
       }
     }
   }
 
-  // O += P V over the 16 keys. o[j] is the m16n8 tile whose column x is head dimension
-  // x * (D / 8) + j.
-  static __device__ __forceinline__ void values(const uint8_t* st, const uint32_t (&pa)[4], float (&o)[D / 8][4],
-                                                const bool (&v_ok)[4]) {
+  // O^T += V^T P^T over 16 keys; pb[x] the P^T fragment of query rows 8x .. 8x+7. Lane row g of
+  // o[x][i] is head dimension g * (D / 8) + 2i, lane row g + 8 the next one.
+  template <bool kHalf>
+  static __device__ __forceinline__ void values(const uint8_t* st, int sub, const uint32_t (&pb)[NT][2],
+                                                float (&o)[NT][D / 16][4], uint32_t live, int ref) {
     const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
     const uint8_t* vt = st + F::kTileBytes;
-    const uint8_t* sc = st + 2 * F::kTileBytes + 64;
-    const int rows[4] = {2 * c, 2 * c + 1, 2 * c + 8, 2 * c + 9};
+    const uint8_t* sc = st + 2 * F::kTileBytes + F::kScaleBytes;
+    const int r0 = 16 * sub + 2 * c;
+    const int rows[4] = {r0, r0 + 1, r0 + 8, r0 + 9};
     constexpr int kBytes = F::kRowBytes / 8;  // this lane's bytes of a row
     constexpr int kW = kBytes / 4;
+    constexpr int kPer = D / 8 / kW;          // elements per word
     uint32_t w[4][kW];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -258,48 +485,37 @@ struct Warp {
       const int blk = g * (D / 8) / kMxBlock;
       uint32_t f[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) f[r] = v_ok[r] ? raw_factor<FMT>(scale_byte(sc, rows[r], blk)) : 0u;
+      for (int r = 0; r < 4; ++r)
+        f[r] = code_factor<FMT, kHalf>(live >> rows[r] & 1 ? sc[rows[r] * F::kScaleRow + blk] : ref, ref);
       f01 = f[0] | (f[1] << 16);
       f23 = f[2] | (f[3] << 16);
     }
 #pragma unroll
-    for (int x = 0; x < kW; ++x) {
-      // the low and high halves of the word, of two keys side by side
-      const uint32_t a0 = __byte_perm(w[0][x], w[1][x], 0x5410), a1 = __byte_perm(w[0][x], w[1][x], 0x7632);
-      const uint32_t b0 = __byte_perm(w[2][x], w[3][x], 0x5410), b1 = __byte_perm(w[2][x], w[3][x], 0x7632);
-      if constexpr (FMT == RING_ATTN_CACHE_BF16) {
-        mma16816(o[2 * x], pa, a0, b0);
-        mma16816(o[2 * x + 1], pa, a1, b1);
-      } else if constexpr (FMT == RING_ATTN_CACHE_MXFP8) {
-        mma16816(o[4 * x], pa, mul_bf16x2(e4m3_raw<false>(a0), f01), mul_bf16x2(e4m3_raw<false>(b0), f23));
-        mma16816(o[4 * x + 1], pa, mul_bf16x2(e4m3_raw<true>(a0), f01), mul_bf16x2(e4m3_raw<true>(b0), f23));
-        mma16816(o[4 * x + 2], pa, mul_bf16x2(e4m3_raw<false>(a1), f01), mul_bf16x2(e4m3_raw<false>(b1), f23));
-        mma16816(o[4 * x + 3], pa, mul_bf16x2(e4m3_raw<true>(a1), f01), mul_bf16x2(e4m3_raw<true>(b1), f23));
-      } else {
-        mma16816(o[8 * x], pa, mul_bf16x2(e2m1_raw<0>(a0), f01), mul_bf16x2(e2m1_raw<0>(b0), f23));
-        mma16816(o[8 * x + 1], pa, mul_bf16x2(e2m1_raw<1>(a0), f01), mul_bf16x2(e2m1_raw<1>(b0), f23));
-        mma16816(o[8 * x + 2], pa, mul_bf16x2(e2m1_raw<2>(a0), f01), mul_bf16x2(e2m1_raw<2>(b0), f23));
-        mma16816(o[8 * x + 3], pa, mul_bf16x2(e2m1_raw<3>(a0), f01), mul_bf16x2(e2m1_raw<3>(b0), f23));
-        mma16816(o[8 * x + 4], pa, mul_bf16x2(e2m1_raw<0>(a1), f01), mul_bf16x2(e2m1_raw<0>(b1), f23));
-        mma16816(o[8 * x + 5], pa, mul_bf16x2(e2m1_raw<1>(a1), f01), mul_bf16x2(e2m1_raw<1>(b1), f23));
-        mma16816(o[8 * x + 6], pa, mul_bf16x2(e2m1_raw<2>(a1), f01), mul_bf16x2(e2m1_raw<2>(b1), f23));
-        mma16816(o[8 * x + 7], pa, mul_bf16x2(e2m1_raw<3>(a1), f01), mul_bf16x2(e2m1_raw<3>(b1), f23));
+    for (int y = 0; y < kW; ++y) {
+      uint32_t b0[kPer], b1[kPer];
+      key_pairs<FMT, kHalf>(w[0][y], w[1][y], f01, b0);
+      key_pairs<FMT, kHalf>(w[2][y], w[3][y], f23, b1);
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) {
+        const uint32_t a[4] = {b0[e], b0[e + 1], b1[e], b1[e + 1]};
+#pragma unroll
+        for (int x = 0; x < NT; ++x) mma16816<kHalf>(o[x][(kPer * y + e) / 2], a, pb[x][0], pb[x][1]);
       }
     }
   }
 };
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::kPerSm) tree_rows_kernel(const Params p) {
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_kernel(const Params p) {
   using F = Fmt<FMT, D>;
-  using W = Warp<FMT, D>;
+  using W = Warp<FMT, D, NT>;
+  constexpr int kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_anc[kMaxNodes], s_vis[kMaxNodes];
   __shared__ int s_depth[kMaxNodes], s_jump[kMaxNodes];
   __shared__ int64_t s_plan[4];
-  __shared__ float s_ml[kWarps][kRows][2];
+  __shared__ float s_ml[kWarps][kRows][3];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
-  const float lift = F::kMx ? kLift : 0.f;
 
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = RING_ATTN_OK;  // the merge kernel reports
   if (warp == 0) {
@@ -335,10 +551,6 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::kPerSm) tree_rows_kerne
       fresh = true;
       continue;
     }
-    if (fresh) {
-      tree_masks(p, b, ks, s_anc, s_vis, s_depth, s_jump);
-      fresh = false;
-    }
     const int64_t local = x - before;
     const int64_t u_local = local / per;
     const int grp = (int)(u_local % p.groups), kvh = (int)(u_local / p.groups);
@@ -348,192 +560,270 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::kPerSm) tree_rows_kerne
     const int64_t head_row = ((int64_t)b * p.c.Hkv + kvh) * p.c.capacity;
     const int live_rows = ks.cnt * p.rep;
 
-    // queries of rows g and g + 8 in the score product's order of head dimensions
-    uint32_t q[F::kKSteps][4];
-    int row_t[2];
-    bool row_live[2];
+    // this warp's steps: one of every quad (the last quad of a unit may be short of some)
+    const int quads = q1 - q0;
+    auto step_of = [&](int j) { return p.quad * (q0 + j) + warp; };
+    auto prefetch = [&](int j) {
+      if (j < quads && step_of(j) < ks.steps)
+        W::load(p, ks, head_row, step_key(p, ks, step_of(j)), ring + (j % F::kStages) * F::kStageBytes);
+      cp_commit();
+    };
+#pragma unroll 1
+    for (int j = 0; j < F::kStages - 1; ++j) prefetch(j);
+    if (fresh) {
+      tree_masks(p, b, ks, s_anc, s_vis, s_depth, s_jump);
+      fresh = false;
+    }
+
+    // queries in the score product's order of head dimensions (lane column g: query row g of
+    // the tile); fp16 ones times 2^(14 - exponent of the row's largest)
+    uint32_t q[NT][F::kKSteps][2];
+    float own_scale[NT];  // scores of query row 8x + g to the base-2 domain, K's step reference apart
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = grp * kRows + g + 8 * r;
-      row_live[r] = row < live_rows;
-      row_t[r] = row_live[r] ? row / p.rep : 0;
-      const uint16_t* src = p.q + b * p.qs_b + (int64_t)(kvh * p.rep + (row_live[r] ? row % p.rep : 0)) * p.qs_h +
-                            row_t[r] * p.qs_t;
+    for (int i = 0; i < NT; ++i) {
+      const int row = grp * kRows + 8 * i + g;
+      const bool in = row < live_rows;
+      const uint16_t* src = p.q + b * p.qs_b + (int64_t)(kvh * p.rep + (in ? row % p.rep : 0)) * p.qs_h +
+                            (in ? row / p.rep : 0) * p.qs_t;
+      uint32_t top = 0;
 #pragma unroll
       for (int s = 0; s < F::kKSteps; ++s)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t lo = row_live[r] ? src[score_dim<FMT, D>(s, c, h, 0)] : 0;
-          const uint32_t hi = row_live[r] ? src[score_dim<FMT, D>(s, c, h, 1)] : 0;
-          const uint32_t v = lo | (hi << 16);
-          q[s][2 * h + r] = F::kMx ? mul_bf16x2(v, 0x5e805e80u) : v;  // 2^62
+          const uint32_t v = in ? *reinterpret_cast<const uint32_t*>(src + score_dim<FMT, D>(s, c, h, 0)) : 0u;
+          q[i][s][h] = v;
+          top = max(top, max(v & 0x7fffu, v >> 16 & 0x7fffu));
         }
+      own_scale[i] = p.scale_log2;
+      if (F::kMx) {
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max((int)(top >> 7), 15) - 127;  // exponent of the largest (not below 2^-112)
+        const float up = pow2(14 - e);
+#pragma unroll
+        for (int s = 0; s < F::kKSteps; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t v = q[i][s][h];
+            q[i][s][h] = pack_f16x2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+          }
+        own_scale[i] = p.scale_log2 * exp2f((float)(e - 14 - lift_code<FMT>()));
+      }
     }
-    // first key of each row's window and the drafted nodes it sees
-    int lo_key[2];
-    uint64_t vis[2];
+    // this lane's query rows in a score tile: 8i + 2c and the next one
+    float row_scale[NT][2];
+    int lo_key[NT][2];      // first key of the row's window
+    uint64_t vis[NT][2];    // drafted nodes it sees
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      lo_key[r] = p.window > 0 ? ks.n + s_depth[row_t[r]] - p.window + 1 : 0;
-      vis[r] = s_vis[row_t[r]];
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        row_scale[i][r] = __shfl_sync(0xffffffffu, own_scale[i], 4 * (2 * c + r));
+        const int row = grp * kRows + 8 * i + 2 * c + r;
+        const int t = row < live_rows ? row / p.rep : 0;
+        lo_key[i][r] = p.window > 0 ? ks.n + s_depth[t] - p.window + 1 : 0;
+        vis[i][r] = s_vis[t];
+      }
+
+    float o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][d][e] = 0.f;
+      m[i][0] = m[i][1] = -INFINITY;
+      l[i][0] = l[i][1] = 0.f;
     }
+    int v_ref = 0;  // E, see the head of the file
 
-    float o[D / 8][4];
-#pragma unroll
-    for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-    const int quads = q1 - q0;
-    auto step_of = [&](int j) { return p.quad * (q0 + j) + warp; };
-#pragma unroll 1
-    for (int j = 0; j < F::kStages - 1; ++j)
-      W::load(p, ks, head_row, step_of(j), j < quads && step_of(j) < ks.steps, ring + j * F::kStageBytes);
 #pragma unroll 1
     for (int j = 0; j < quads; ++j) {
-      {
-        const int a = j + F::kStages - 1;
-        W::load(p, ks, head_row, step_of(a), a < quads && step_of(a) < ks.steps,
-                ring + (a % F::kStages) * F::kStageBytes);
-      }
+      prefetch(j + F::kStages - 1);
       cp_wait<F::kStages - 1>();
       __syncwarp();
-      const int i = step_of(j);
-      if (i < ks.steps) {
+      const int i_step = step_of(j);
+      if (i_step < ks.steps) {
         const uint8_t* st = ring + (j % F::kStages) * F::kStageBytes;
-        const int kb = step_key(p, ks, i);
-        // every row sees all 16 keys
-        const bool whole = kb + kStep <= ks.n &&
-                           (p.window <= 0 || kb + kStep <= p.sinks || (int64_t)kb >= (int64_t)ks.n + p.T - p.window);
-        bool k_ok[2] = {true, true}, v_ok[4] = {true, true, true, true};
-        if (F::kMx && !whole) {
+        const int kb = step_key(p, ks, i_step);
+        // every row sees all keys of the step
+        const bool whole =
+            kb + F::kStep <= ks.n &&
+            (p.window <= 0 || kb + F::kStep <= p.sinks || (int64_t)kb >= (int64_t)ks.n + p.T - p.window);
+        uint32_t live = 0xffffffffu;
+        int ref[2] = {0, 0};
+        bool half = true;
+        float p_up = 1.f, k_up = 1.f;
+        if (F::kMx) {
+          if (!whole) live = __ballot_sync(0xffffffffu, lane < F::kStep && key_live(p, ks, kb + lane));
+          int low[2];
+          W::scale_range(st, live, ref, low);
+          half = ref[0] < 255 && ref[1] < 255 && ref[0] - low[0] <= kSpread && ref[1] - low[1] <= kSpread;
+          ref[0] = min(ref[0], 254);
+          ref[1] = min(ref[1], 254);
+          if (ref[1] > v_ref) {  // raise E: O carries 2^-E
+            const float a = pow2(v_ref - ref[1]);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) k_ok[t] = key_live(p, ks, kb + 8 * t + g);
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) v_ok[t] = key_live(p, ks, kb + 2 * c + (t & 1) + 8 * (t >> 1));
+              for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][d][e] *= a;
+            v_ref = ref[1];
+          }
+          half = half && v_ref - ref[1] <= kBelow;
+          p_up = pow2(ref[1] - v_ref + kLiftP);
+          k_up = pow2(ref[0] - 127);
         }
-        float s[2][4];
-        W::scores(st, q, s, k_ok);
+#pragma unroll 1
+        for (int sub = 0; sub < F::kSubs; ++sub) {
+          float s[NT][4];  // (key g, rows 2c, 2c+1), (key g + 8, the same rows)
+          if (half || !F::kMx)
+            W::template scores<F::kMx>(st, sub, q, s, live, ref[0]);
+          else
+            W::template scores<false>(st, sub, q, s, live, ref[0]);
+          bool rise = false;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+          for (int i = 0; i < NT; ++i) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][e] *= p.scale_log2;
-        if (!whole) {
+            for (int e = 0; e < 4; ++e) s[i][e] *= k_up * row_scale[i][e & 1];
+            if (!whole) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = e / 2;
-              const int u = kb + 8 * t + 2 * c + (e & 1);
-              const bool see = u < ks.n ? (u < p.sinks || u >= lo_key[r])
-                                        : (u < ks.n + ks.cnt && (vis[r] >> (u - ks.n) & 1));
-              if (!see) s[t][e] = -INFINITY;
-            }
-        }
-        // the reference maximum moves only when a score passes it by kRescale (or is the first)
-        const float m0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        const float m1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-        if (__any_sync(0xffffffffu, m0 > m[0] + kRescale || m1 > m[1] + kRescale)) {
-          float top[2] = {m0, m1};
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-            if (top[r] > m[r]) {
-              const float a = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - top[r]);
-              m[r] = top[r];
-              l[r] *= a;
-#pragma unroll
-              for (int d = 0; d < D / 8; ++d) {
-                o[d][2 * r] *= a;
-                o[d][2 * r + 1] *= a;
+              for (int e = 0; e < 4; ++e) {
+                const int r = e & 1, u = kb + 16 * sub + g + 8 * (e >> 1);
+                const bool see = u < ks.n ? (u < p.sinks || u >= lo_key[i][r])
+                                          : (u < ks.n + ks.cnt && (vis[i][r] >> (u - ks.n) & 1));
+                if (!see) s[i][e] = -INFINITY;
               }
             }
-          }
-        }
-        uint32_t pa[4];
-        const float z0 = m[0] == -INFINITY ? 0.f : m[0] - lift, z1 = m[1] == -INFINITY ? 0.f : m[1] - lift;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float p0 = ex2_approx(s[t][0] - z0), p1 = ex2_approx(s[t][1] - z0);
-          const float p2 = ex2_approx(s[t][2] - z1), p3 = ex2_approx(s[t][3] - z1);
-          l[0] += p0 + p1;
-          l[1] += p2 + p3;
-          pa[2 * t] = pack_bf16x2(p0, p1);
-          pa[2 * t + 1] = pack_bf16x2(p2, p3);
+            for (int r = 0; r < 2; ++r) rise |= fmaxf(s[i][r], s[i][r + 2]) > m[i][r] + rescale_log2<FMT>();
+          }
+          // the reference maximum moves only when a score passes it by rescale_log2 (or is the first)
+          if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                float top = fmaxf(s[i][r], s[i][r + 2]);
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                if (top > m[i][r]) {
+                  const float a = m[i][r] == -INFINITY ? 0.f : ex2_approx(m[i][r] - top);
+                  m[i][r] = top;
+                  l[i][r] *= a;
+#pragma unroll
+                  for (int d = 0; d < D / 16; ++d) {
+                    o[i][d][r] *= a;
+                    o[i][d][r + 2] *= a;
+                  }
+                }
+              }
+          }
+          uint32_t pb[NT][2];
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const float z0 = m[i][0] == -INFINITY ? 0.f : m[i][0], z1 = m[i][1] == -INFINITY ? 0.f : m[i][1];
+            const float p0 = ex2_approx(s[i][0] - z0), p1 = ex2_approx(s[i][1] - z1);
+            const float p2 = ex2_approx(s[i][2] - z0), p3 = ex2_approx(s[i][3] - z1);
+            l[i][0] += p0 + p2;
+            l[i][1] += p1 + p3;
+            uint32_t a, d;
+            if (F::kMx && half) {
+              a = pack_f16x2(p0 * p_up, p1 * p_up);
+              d = pack_f16x2(p2 * p_up, p3 * p_up);
+            } else {
+              a = pack_bf16x2(p0 * p_up, p1 * p_up);
+              d = pack_bf16x2(p2 * p_up, p3 * p_up);
+            }
+            pb[i][0] = transpose8(a);  // (keys 2c, 2c + 1, query row g)
+            pb[i][1] = transpose8(d);
+          }
+          if (half || !F::kMx)
+            W::template values<F::kMx>(st, sub, pb, o, live, ref[1]);
+          else
+            W::template values<false>(st, sub, pb, o, live, ref[1]);
         }
-        W::values(st, pa, o, v_ok);
       }
       __syncwarp();
     }
     cp_wait<0>();
 
-    // join the four warps' states: weights 2^(m_w - M), then O / l
+    // join the four warps' states: weights 2^(m_w - M), and 2^E_w on what carries it, then O / l
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (c == 0) {
-        s_ml[warp][g + 8 * r][0] = m[r];
-        s_ml[warp][g + 8 * r][1] = l[r];
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float y = l[i][r];
+        y += __shfl_xor_sync(0xffffffffu, y, 4);
+        y += __shfl_xor_sync(0xffffffffu, y, 8);
+        y += __shfl_xor_sync(0xffffffffu, y, 16);
+        if (g == 0) {
+          s_ml[warp][8 * i + 2 * c + r][0] = m[i][r];
+          s_ml[warp][8 * i + 2 * c + r][1] = y;
+          s_ml[warp][8 * i + 2 * c + r][2] = F::kMx ? (float)(v_ref - 127 - kLiftP - lift_code<FMT>()) : 0.f;
+        }
       }
-    }
     __syncthreads();  // every warp has left its ring: the O tiles take its place
     float* so = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float* dst = so + (warp * kRows + g + 8 * r) * (D + 4) + (2 * c + e) * (D / 8);
+      for (int r = 0; r < 2; ++r) {
+        float* dst = so + (warp * kRows + 8 * i + 2 * c + r) * (D + 4) + g * (D / 8);
 #pragma unroll
-        for (int j = 0; j < D / 8; j += 4)
-          *reinterpret_cast<float4*>(dst + j) =
-              make_float4(o[j][2 * r + e], o[j + 1][2 * r + e], o[j + 2][2 * r + e], o[j + 3][2 * r + e]);
+        for (int d = 0; d < D / 16; d += 2)
+          *reinterpret_cast<float4*>(dst + 2 * d) =
+              make_float4(o[i][d][r], o[i][d][r + 2], o[i][d + 1][r], o[i][d + 1][r + 2]);
       }
     __syncthreads();
     const bool alone = q0 == 0 && q1 == per;  // the unit's only part
     const int64_t slot = (int64_t)blockIdx.x + unit;
     {
-      const int r = threadIdx.x / 8, d0 = (threadIdx.x % 8) * (D / 8);
+      constexpr int kTpr = kThreads / kRows, kPer = D / kTpr;  // threads and dimensions per row
+      const int r = threadIdx.x / kTpr, d0 = (threadIdx.x % kTpr) * kPer;
       const int row = grp * kRows + r;
       if (row < live_rows) {
-        float M = -INFINITY;
+        float M = -INFINITY, E = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w][r][0]);
-        float L = 0.f, acc[D / 8];
+        for (int w = 0; w < kWarps; ++w) {
+          M = fmaxf(M, s_ml[w][r][0]);
+          E = fmaxf(E, s_ml[w][r][2]);
+        }
+        float L = 0.f, acc[kPer];
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) acc[e] = 0.f;
+        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float mw = s_ml[w][r][0];
           if (mw == -INFINITY) continue;
           const float a = ex2_approx(mw - M);
           L += a * s_ml[w][r][1];
+          const float av = a * exp2f(s_ml[w][r][2] - E);
           const float* src = so + (w * kRows + r) * (D + 4) + d0;
 #pragma unroll
-          for (int e = 0; e < D / 8; ++e) acc[e] = fmaf(a, src[e], acc[e]);
+          for (int e = 0; e < kPer; ++e) acc[e] = fmaf(av, src[e], acc[e]);
         }
-        // held values are 2^-lift of the true ones, l is 2^lift of its own
         const bool none = M == -INFINITY;
-        const float inv = none ? 0.f : exp2f(lift) / L;
-        const float lse2 = none ? -INFINITY : M + log2f(L) - lift;
+        const float inv = none ? 0.f : 1.f / L;
+        const float up = exp2f(E);  // applied apart from 1 / L: the two together may leave fp32's range
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * inv * up;
+        const float lse2 = none ? -INFINITY : M + log2f(L);
         if (alone) {
           const int64_t orow = out_row(p, b, kvh, row);
-          uint32_t pk[D / 16];
 #pragma unroll
-          for (int e = 0; e < D / 16; ++e) pk[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + d0);
-#pragma unroll
-          for (int e = 0; e < D / 64; ++e)
-            dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+          for (int e = 0; e < kPer; e += 4)
+            *reinterpret_cast<uint2*>(p.out + orow * D + d0 + e) =
+                make_uint2(pack_bf16x2(acc[e], acc[e + 1]), pack_bf16x2(acc[e + 2], acc[e + 3]));
           if (d0 == 0) p.lse[orow] = lse2 * 0.69314718055994530942f;
         } else {
           float* dst = p.o_parts + (slot * kRows + r) * D + d0;
 #pragma unroll
-          for (int e = 0; e < D / 8; e += 4)
-            *reinterpret_cast<float4*>(dst + e) =
-                make_float4(acc[e] * inv, acc[e + 1] * inv, acc[e + 2] * inv, acc[e + 3] * inv);
+          for (int e = 0; e < kPer; e += 4)
+            *reinterpret_cast<float4*>(dst + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
           if (d0 == 0) p.lse_parts[slot * kRows + r] = lse2;
         }
       }
@@ -646,29 +936,27 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const Params p) {
   if (d4 == 0) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(tot)) * 0.69314718055994530942f;
 }
 
-template <int FMT, int D>
-int launch_rows(const Params& p, cudaStream_t stream) {
-  constexpr int smem = Fmt<FMT, D>::kSmem;
-  if (cudaFuncSetAttribute(tree_rows_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+template <int FMT, int D, int NT>
+int launch_rows_t(const Params& p, cudaStream_t stream) {
+  constexpr int smem = Fmt<FMT, D>::smem(8 * NT);
+  auto kern = tree_rows_kernel<FMT, D, NT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return RING_ATTN_ECUDA;
-  tree_rows_kernel<FMT, D><<<p.ctas, kThreads, smem, stream>>>(p);
+  kern<<<p.ctas, kThreads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
 }
 
-inline int ctas_per_sm(int format, int D) {
-  switch (format) {
-    case RING_ATTN_CACHE_BF16:
-      return D == 64 ? Fmt<RING_ATTN_CACHE_BF16, 64>::kPerSm : Fmt<RING_ATTN_CACHE_BF16, 128>::kPerSm;
-    case RING_ATTN_CACHE_MXFP8:
-      return D == 64 ? Fmt<RING_ATTN_CACHE_MXFP8, 64>::kPerSm : Fmt<RING_ATTN_CACHE_MXFP8, 128>::kPerSm;
-    default: return D == 64 ? Fmt<RING_ATTN_CACHE_MXFP4, 64>::kPerSm : Fmt<RING_ATTN_CACHE_MXFP4, 128>::kPerSm;
-  }
+template <int FMT, int D>
+int launch_rows(const Params& p, cudaStream_t stream) {
+  return p.rows_per_group == 8 ? launch_rows_t<FMT, D, 1>(p, stream) : launch_rows_t<FMT, D, 2>(p, stream);
 }
 
 template <int FMT>
 int launch_rows_d(const Params& p, cudaStream_t stream) {
   return p.c.D == 64 ? launch_rows<FMT, 64>(p, stream) : launch_rows<FMT, 128>(p, stream);
 }
+
+inline int step_keys(int format, int D) { return format == RING_ATTN_CACHE_BF16 && D == 128 ? 16 : 32; }
 
 }  // namespace tree
 
@@ -682,11 +970,11 @@ struct TreePlan {
 
 TreePlan tree_plan(const CacheView& c, int Hq, int T) {
   TreePlan t;
-  t.rows_per_group = tree::kRows;
+  t.rows_per_group = T * (Hq / c.Hkv) <= 8 ? 8 : 16;
   t.groups = (T * (Hq / c.Hkv) + t.rows_per_group - 1) / t.rows_per_group;
-  t.step = tree::kStep;
+  t.step = tree::step_keys(c.format, c.D);
   t.quad = tree::kWarps;
-  t.ctas = 148 * tree::ctas_per_sm(c.format, c.D);
+  t.ctas = 148 * (c.D == 128 && t.rows_per_group == 16 ? 2 : 3);
   t.min_quads = 2;
   t.units = (int64_t)c.B * c.Hkv * t.groups;
   t.slots = t.ctas + t.units;

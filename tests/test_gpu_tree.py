@@ -5,7 +5,9 @@ E = scale sum |q||k|): each weight p is rounded to bf16 for its product (2^-8 A)
 once more (2^-8 |O| <= 2^-8 A); a score is a sum of D products accumulated in fp32, off by at
 most D 2^-23 E (twice the half-step bound, for a truncating adder), and enters a weight and
 the weights' sum (2 D 2^-23 E A); 2^x is good to 2^-22, sums and rescales to a few 2^-23 (the
-2^-16 covers them at these lengths).
+2^-16 covers them at these lengths). A microscaled cache may be read with the weights in fp16
+(11 bits, better than bf16's 8) scaled so that its smallest step is 2^-34: a weight below 2^-24 is
+off by at most 2^-35 of the row's largest, which adds 2^-35 |v| per key, whatever A is.
 """
 import numpy as np
 import pytest
@@ -22,14 +24,14 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
-def check(out, lse, ref, D, what=""):
+def check(out, lse, ref, D, what="", floor=0.0):
     O, L, A, E = ref
     o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
     seen = np.isfinite(L)
     assert (np.isneginf(l) == ~seen).all(), what
     assert (o[~seen] == 0).all(), what
     es = D * 2.0 ** -23 * E + 2.0 ** -16
-    tol = A * (2.0 ** -8 + 2.0 ** -8 + 2 * es[..., None]) + 2.0 ** -126
+    tol = A * (2.0 ** -8 + 2.0 ** -8 + 2 * es[..., None]) + 2.0 ** -126 + floor
     assert np.isfinite(o).all(), what
     worst = (np.abs(o - O) / tol).max()
     assert worst <= 1, f"{what}: out off by {worst:.2f} of its tolerance"
@@ -63,7 +65,16 @@ def random_tree(B, T, seed):
     return [[-1 if i == 0 else int(r.integers(-1, i)) for i in range(T)] for _ in range(B)]
 
 
-def run(q, cache, vals, lengths, parents=None, counts=None, window=0, sinks=0, scale=None, what=""):
+def weight_floor(cache, vals, lengths, T):
+    """2^-35 sum |v| over a sequence's keys, at most (0 for bf16 rows)."""
+    if cache.format == "bf16":
+        return 0.0
+    top = max(np.abs(vals[1][b, :, :n + T]).max(initial=0, where=np.isfinite(vals[1][b, :, :n + T])) * (n + T)
+              for b, n in enumerate(lengths))
+    return 2.0 ** -35 * top
+
+
+def run(q, cache, vals, lengths, parents=None, counts=None, window=0, sinks=0, scale=None, what="", floor=None):
     D = q.shape[-1]
     ws = tree_workspace(q, cache)
     out, lse = tree_attention(q, cache, i32(lengths), None if parents is None else i32(parents),
@@ -71,7 +82,7 @@ def run(q, cache, vals, lengths, parents=None, counts=None, window=0, sinks=0, s
     assert status(ws) == 0
     ref = oracle.tree_reference(q.double().cpu().numpy(), *vals, lengths, parents, counts, window, sinks,
                                 1 / np.sqrt(D) if scale is None else scale)
-    check(out, lse, ref, D, what)
+    check(out, lse, ref, D, what, weight_floor(cache, vals, lengths, q.shape[2]) if floor is None else floor)
     return out, lse
 
 
@@ -143,12 +154,22 @@ def test_large_scores_and_far_scales(cuda_lib):
             cache_write(cache, k.cuda(), v.cuda(), i32([0]))
             vals = [t.double().cpu().numpy() for t in cache_read(cache, i32([0]), 64, dtype=torch.float32)]
             q = (torch.randn(1, 2, 1, 64, generator=g) * (2.0 ** -e if e > -100 else 1.0)).bfloat16().cuda()
-            if e == -100:  # V's scales lie above 2^63: its blocks count as NaN, the scores are as they were
-                out, lse = tree_attention(q, cache, i32([63]))
-                L = oracle.tree_reference(q.double().cpu().numpy(), *vals, [63], None, None, 0, 0, 1 / 8)[1]
-                assert out.isnan().all() and np.abs(lse.double().cpu().numpy() - L).max() <= 2.0 ** -15
-                continue
             run(q, cache, vals, [63], what=f"{fmt} 2^{e}")
+    # scales of one step far apart: rows and blocks 2^-40 .. 2^40 of one another, the largest values with small weights
+    for fmt in ("mxfp8", "mxfp4"):
+        cache = KVCache.allocate(1, 1, 96, 128, fmt)
+        k, v = torch.randn(1, 1, 96, 128, generator=g), torch.randn(1, 1, 96, 128, generator=g)
+        v[0, 0, 5] *= 2.0 ** 40
+        k[0, 0, 5] = 0.0
+        v[0, 0, 40:] *= torch.exp2(torch.arange(56.0) - 40)[:, None]
+        v[0, 0, 20, 32:64] *= 2.0 ** -30
+        k[0, 0, 21, 64:] *= 2.0 ** -40
+        k[0, 0, 50:52] *= 2.0 ** -20
+        cache_write(cache, k.cuda(), v.cuda(), i32([0]))
+        vals = [t.double().cpu().numpy() for t in cache_read(cache, i32([0]), 96, dtype=torch.float32)]
+        q = (8 * torch.randn(1, 4, 2, 128, generator=g)).bfloat16().cuda()
+        run(q, cache, vals, [90], what=f"{fmt} mixed scales", floor=0.0)
+        run(q, cache, vals, [4], what=f"{fmt} mixed scales, short", floor=0.0)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
