@@ -40,6 +40,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "sm100_ptx.cuh"
 #include "tree_common.cuh"
 
@@ -249,13 +251,23 @@ __host__ __device__ constexpr int lift_code() {
   return FMT == RING_ATTN_CACHE_MXFP8 ? 7 : 1;
 }
 
-// 2^(byte - ref + lift) for an fp16 pair's half, or the same times 2^120 or 2^126 for the
-// bf16 form (NaN for a block that is not finite, 0 far below the reference).
+// The factor 2^(byte - ref + lift) of two codes, `lo` and `hi` their blocks' scale bytes: as
+// two fp16 (fields (byte - ref + lift + 15) << 10, built by one multiply-add per byte), or
+// times 2^120 or 2^126 as two bf16 for the bf16 form (NaN for a block that is not finite, 0
+// far below the reference).
 template <int FMT, bool kHalf>
-__device__ __forceinline__ uint32_t code_factor(int byte, int ref) {
-  if (kHalf) return (uint32_t)(byte - ref + lift_code<FMT>() + 15) << 10;
-  const int e = byte - ref + lift_code<FMT>() + (FMT == RING_ATTN_CACHE_MXFP8 ? 120 : 126) + 127;
-  return byte == 255 ? 0x7fc0u : (e <= 0 ? 0u : (uint32_t)e << 7);
+__device__ __forceinline__ uint32_t code_factors(uint32_t lo, uint32_t hi, int ref) {
+  if (kHalf) return lo * 0x400u + hi * 0x4000000u + (uint32_t)(lift_code<FMT>() + 15 - ref) * 0x4000400u;
+  auto one = [&](int byte) {
+    const int e = byte - ref + lift_code<FMT>() + (FMT == RING_ATTN_CACHE_MXFP8 ? 120 : 126) + 127;
+    return byte == 255 ? 0x7fc0u : (e <= 0 ? 0u : (uint32_t)e << 7);
+  };
+  return one((int)lo) | (one((int)hi) << 16);
+}
+template <int FMT, bool kHalf>
+__device__ __forceinline__ uint32_t code_factor(uint32_t byte, int ref) {
+  if (kHalf) return byte * 0x4000400u + (uint32_t)(lift_code<FMT>() + 15 - ref) * 0x4000400u;
+  return code_factors<FMT, false>(byte, byte, ref);
 }
 
 // Chunk positions inside a row of the ring (16-byte units) that keep the fragment loads
@@ -337,30 +349,33 @@ struct Warp {
   }
 
   // The largest and smallest scale bytes of the step's live K rows (ref[0], low[0]) and V rows
-  // (ref[1], low[1]).
-  static __device__ __forceinline__ void scale_range(const uint8_t* st, uint32_t live_rows, int (&ref)[2],
+  // (ref[1], low[1]). Dead rows hold zero codes under scale bytes that may be anything: theirs
+  // become the reference, so that no factor is out of range.
+  static __device__ __forceinline__ void scale_range(uint8_t* st, bool all_live, uint32_t live_rows, int (&ref)[2],
                                                      int (&low)[2]) {
+    using Word = typename std::conditional<F::kScaleRow == 4, uint32_t, uint16_t>::type;
     const int lane = threadIdx.x % 32;
-    const bool mine = F::kStep == 32 ? (live_rows >> lane & 1) : (lane < 16 && (live_rows >> lane & 1));
+    const bool mine = all_live || (live_rows >> lane & 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint8_t* sc = st + 2 * F::kTileBytes + i * F::kScaleBytes;
-      uint32_t hi = 0, lo = 255;
-      if (mine) {
-        if (F::kScaleRow == 4) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
-          const uint32_t a = w & 0x00ff00ffu, b = w >> 8 & 0x00ff00ffu;
-          const uint32_t mx = __vmaxu2(a, b), mn = __vminu2(a, b);
-          hi = max(mx & 0xffffu, mx >> 16);
-          lo = min(mn & 0xffffu, mn >> 16);
-        } else {
-          const uint32_t w = *reinterpret_cast<const uint16_t*>(sc + lane * 2);
-          hi = max(w & 255u, w >> 8);
-          lo = min(w & 255u, w >> 8);
-        }
+      Word* sc = reinterpret_cast<Word*>(st + 2 * F::kTileBytes + i * F::kScaleBytes) + lane;
+      const uint32_t w = *sc;
+      uint32_t hi, lo;
+      if (F::kScaleRow == 4) {
+        const uint32_t a = w & 0x00ff00ffu, b = w >> 8 & 0x00ff00ffu;
+        const uint32_t mx = __vmaxu2(a, b), mn = __vminu2(a, b);
+        hi = max(mx & 0xffffu, mx >> 16);
+        lo = min(mn & 0xffffu, mn >> 16);
+      } else {
+        hi = max(w & 255u, w >> 8);
+        lo = min(w & 255u, w >> 8);
       }
-      ref[i] = (int)__reduce_max_sync(0xffffffffu, hi);
-      low[i] = (int)__reduce_min_sync(0xffffffffu, lo);
+      ref[i] = (int)__reduce_max_sync(0xffffffffu, mine ? hi : 0u);
+      low[i] = (int)__reduce_min_sync(0xffffffffu, mine ? lo : 255u);
+      if (!all_live) {
+        if (!mine) *sc = (Word)(min(ref[i], 254) * 0x01010101u);
+        __syncwarp();
+      }
     }
   }
 
@@ -374,11 +389,10 @@ struct Warp {
   }
 
   // Scores of 16 keys (16 sub .. 16 sub + 15 of the step): s[x] the m16n8 tile of query rows
-  // 8x .. 8x+7. live: bits of the rows that hold data (a dead row's codes are zeros, its scale
-  // bytes anything).
+  // 8x .. 8x+7.
   template <bool kHalf>
   static __device__ __forceinline__ void scores(const uint8_t* st, int sub, const uint32_t (&q)[NT][F::kKSteps][2],
-                                                float (&s)[NT][4], uint32_t live, int ref) {
+                                                float (&s)[NT][4], int ref) {
     const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
     const int row0 = 16 * sub + g, row1 = row0 + 8;
     const uint8_t* k0 = st + row0 * F::kRowBytes;
@@ -388,10 +402,7 @@ struct Warp {
     for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
-    auto factor = [&](int row, int blk) {
-      const int byte = live >> row & 1 ? sc[row * F::kScaleRow + blk] : ref;
-      return code_factor<FMT, kHalf>(byte, ref) * 0x10001u;
-    };
+    auto factor = [&](int row, int blk) { return code_factor<FMT, kHalf>(sc[row * F::kScaleRow + blk], ref); };
     if constexpr (FMT == RING_ATTN_CACHE_BF16) {
 #pragma unroll
       for (int i = 0; i < F::kKSteps / 2; ++i) {
@@ -453,7 +464,7 @@ struct Warp {
   // o[x][i] is head dimension g * (D / 8) + 2i, lane row g + 8 the next one.
   template <bool kHalf>
   static __device__ __forceinline__ void values(const uint8_t* st, int sub, const uint32_t (&pb)[NT][2],
-                                                float (&o)[NT][D / 16][4], uint32_t live, int ref) {
+                                                float (&o)[NT][D / 16][4], int ref) {
     const int lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
     const uint8_t* vt = st + F::kTileBytes;
     const uint8_t* sc = st + 2 * F::kTileBytes + F::kScaleBytes;
@@ -485,10 +496,9 @@ struct Warp {
       const int blk = g * (D / 8) / kMxBlock;
       uint32_t f[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        f[r] = code_factor<FMT, kHalf>(live >> rows[r] & 1 ? sc[rows[r] * F::kScaleRow + blk] : ref, ref);
-      f01 = f[0] | (f[1] << 16);
-      f23 = f[2] | (f[3] << 16);
+      for (int r = 0; r < 4; ++r) f[r] = sc[rows[r] * F::kScaleRow + blk];
+      f01 = code_factors<FMT, kHalf>(f[0], f[1], ref);
+      f23 = code_factors<FMT, kHalf>(f[2], f[3], ref);
     }
 #pragma unroll
     for (int y = 0; y < kW; ++y) {
@@ -645,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
       __syncwarp();
       const int i_step = step_of(j);
       if (i_step < ks.steps) {
-        const uint8_t* st = ring + (j % F::kStages) * F::kStageBytes;
+        uint8_t* st = ring + (j % F::kStages) * F::kStageBytes;
         const int kb = step_key(p, ks, i_step);
         // every row sees all keys of the step
         const bool whole =
@@ -656,9 +666,9 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
         bool half = true;
         float p_up = 1.f, k_up = 1.f;
         if (F::kMx) {
-          if (!whole) live = __ballot_sync(0xffffffffu, lane < F::kStep && key_live(p, ks, kb + lane));
+          if (!whole) live = __ballot_sync(0xffffffffu, key_live(p, ks, kb + lane));
           int low[2];
-          W::scale_range(st, live, ref, low);
+          W::scale_range(st, whole, live, ref, low);
           half = ref[0] < 255 && ref[1] < 255 && ref[0] - low[0] <= kSpread && ref[1] - low[1] <= kSpread;
           ref[0] = min(ref[0], 254);
           ref[1] = min(ref[1], 254);
@@ -679,10 +689,10 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
 #pragma unroll 1
         for (int sub = 0; sub < F::kSubs; ++sub) {
           float s[NT][4];  // (key g, rows 2c, 2c+1), (key g + 8, the same rows)
-          if (half || !F::kMx)
-            W::template scores<F::kMx>(st, sub, q, s, live, ref[0]);
+          if (!F::kMx || __builtin_expect(half, 1))
+            W::template scores<F::kMx>(st, sub, q, s, ref[0]);
           else
-            W::template scores<false>(st, sub, q, s, live, ref[0]);
+            W::template scores<false>(st, sub, q, s, ref[0]);
           bool rise = false;
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
@@ -741,10 +751,10 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
             pb[i][0] = transpose8(a);  // (keys 2c, 2c + 1, query row g)
             pb[i][1] = transpose8(d);
           }
-          if (half || !F::kMx)
-            W::template values<F::kMx>(st, sub, pb, o, live, ref[1]);
+          if (!F::kMx || __builtin_expect(half, 1))
+            W::template values<F::kMx>(st, sub, pb, o, ref[1]);
           else
-            W::template values<false>(st, sub, pb, o, live, ref[1]);
+            W::template values<false>(st, sub, pb, o, ref[1]);
         }
       }
       __syncwarp();
