@@ -156,60 +156,140 @@ __device__ __forceinline__ int warp_find_sequence(const Params& p, int64_t x, in
   return p.c.B;
 }
 
-// Ancestors of the drafted nodes of sequence b as bit sets (bit t of anc[t] is the node
-// itself), reduced to those that the window and the sinks let node t see, and the nodes'
-// depths. All threads of the CTA call it; anc, vis, depth and jump hold kMaxNodes entries.
-// A parent outside [-1, t) reads as -1 (and is reported by the status word).
-__device__ __forceinline__ void tree_masks(const Params& p, int b, const Keys& k, uint64_t* anc, uint64_t* vis,
-                                           int* depth, int* jump) {
-  const int t = threadIdx.x;
-  const bool mine = t < k.cnt;
-  if (p.parents == nullptr) {
-    if (mine) {
-      anc[t] = t == 63 ? ~0ull : (1ull << (t + 1)) - 1;
-      jump[t] = t - 1;
+// The drafted nodes of a sequence, held by one warp: lane l has nodes l and l + 32. seen: the
+// node itself and its ancestors as bits, reduced to those that the window and the sinks let
+// it see. A parent outside [-1, t) reads as -1 (and is reported by the status word).
+struct Nodes {
+  uint64_t seen[2];
+  int depth[2];
+};
+
+__device__ __forceinline__ Nodes warp_nodes(const Params& p, int b, const Keys& k) {
+  const int lane = threadIdx.x % 32;
+  Nodes x;
+  int jump[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int t = lane + 32 * s;
+    const bool mine = t < k.cnt;
+    jump[s] = -1;
+    if (p.parents == nullptr) {
+      x.seen[s] = !mine ? 0 : (t == 63 ? ~0ull : (1ull << (t + 1)) - 1);
+    } else {
+      x.seen[s] = mine ? 1ull << t : 0;
+      const int par = mine ? p.parents[(int64_t)b * p.T + t] : -1;
+      if (par >= 0 && par < t) jump[s] = par;
     }
-    __syncthreads();
-  } else {
-    if (mine) {
-      const int par = p.parents[(int64_t)b * p.T + t];
-      anc[t] = 1ull << t;
-      jump[t] = par >= -1 && par < t ? par : -1;
-    }
-    __syncthreads();
+  }
+  if (p.parents != nullptr) {
     // pointer doubling: after round i a node's set holds its first 2^i ancestors
     for (int r = 1; r < k.cnt; r <<= 1) {
-      uint64_t add = 0;
-      int next = -1;
-      if (mine && jump[t] >= 0) {
-        add = anc[jump[t]];
-        next = jump[jump[t]];
+      uint64_t add[2];
+      int next[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int from = jump[s] & 31;
+        const uint64_t a0 = __shfl_sync(0xffffffffu, x.seen[0], from), a1 = __shfl_sync(0xffffffffu, x.seen[1], from);
+        const int j0 = __shfl_sync(0xffffffffu, jump[0], from), j1 = __shfl_sync(0xffffffffu, jump[1], from);
+        add[s] = jump[s] < 0 ? 0 : (jump[s] < 32 ? a0 : a1);
+        next[s] = jump[s] < 0 ? -1 : (jump[s] < 32 ? j0 : j1);
       }
-      __syncthreads();
-      if (mine) {
-        anc[t] |= add;
-        jump[t] = next;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        x.seen[s] |= add[s];
+        jump[s] = next[s];
       }
-      __syncthreads();
     }
   }
-  if (mine) depth[t] = __popcll(anc[t]) - 1;
-  __syncthreads();
-  if (mine) {
-    uint64_t v = anc[t];
-    if (p.window > 0 && p.window <= depth[t]) {
-      for (int j = 0; j < t; ++j)
-        if ((v >> j & 1) && depth[j] <= depth[t] - p.window && (int64_t)k.n + depth[j] >= p.sinks) v &= ~(1ull << j);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) x.depth[s] = __popcll(x.seen[s]) - 1;
+  // ancestors that fell out of a window shorter than the tree is deep
+  if (__any_sync(0xffffffffu, p.window > 0 && (p.window <= x.depth[0] || p.window <= x.depth[1]))) {
+    const uint64_t anc[2] = {x.seen[0], x.seen[1]};
+    for (int j = 0; j < k.cnt; ++j) {
+      const int d0 = __shfl_sync(0xffffffffu, x.depth[0], j & 31), d1 = __shfl_sync(0xffffffffu, x.depth[1], j & 31);
+      const int dj = j < 32 ? d0 : d1;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if ((anc[s] >> j & 1) && dj <= x.depth[s] - p.window && (int64_t)k.n + dj >= p.sinks)
+          x.seen[s] &= ~(1ull << j);
     }
-    vis[t] = v;
   }
-  __syncthreads();
+  return x;
+}
+
+// Node t's set and depth (all lanes call it, each with its own t).
+__device__ __forceinline__ void node_of(const Nodes& x, int t, uint64_t& seen, int& depth) {
+  const uint64_t a0 = __shfl_sync(0xffffffffu, x.seen[0], t & 31), a1 = __shfl_sync(0xffffffffu, x.seen[1], t & 31);
+  const int d0 = __shfl_sync(0xffffffffu, x.depth[0], t & 31), d1 = __shfl_sync(0xffffffffu, x.depth[1], t & 31);
+  seen = t < 32 ? a0 : a1;
+  depth = t < 32 ? d0 : d1;
+}
+
+// A CTA's walk over the parts of its share: `part` is set to the next one while there is one.
+struct Part {
+  int b, kvh, grp;
+  Keys ks;
+  int q0, q1;        // quads of the unit
+  bool alone;        // the whole unit
+  int64_t unit;
+  int64_t head_row;  // first cache row of (b, kv head)
+};
+struct Walk {
+  int64_t x, x_end, before;  // next quad, end of the share, quads before sequence b
+  int b;
+};
+
+// Called by one warp; `out` (shared memory) then holds the walk for every thread of the CTA.
+__device__ __forceinline__ void warp_begin_walk(const Params& p, Walk* out) {
+  int64_t total, before = 0, none;
+  warp_totals(p, 0, total, none);
+  const int64_t act = active_ctas(p, total);
+  const int64_t cta = blockIdx.x;
+  const int64_t x0 = cta < act ? share_begin(total, act, cta) : 0;
+  const int64_t x1 = cta < act ? share_begin(total, act, cta + 1) : 0;
+  const int b = x0 < x1 ? warp_find_sequence(p, x0, before) : p.c.B;
+  if (threadIdx.x % 32 == 0) {
+    out->x = x0;
+    out->x_end = x1;
+    out->before = before;
+    out->b = b;
+  }
+}
+
+__device__ __forceinline__ bool next_part(const Params& p, Walk& w, Part& part) {
+  while (w.x < w.x_end) {
+    part.ks = sequence_keys(p, w.b);
+    const int64_t per = (part.ks.steps + p.quad - 1) / p.quad;
+    const int64_t here = per * p.c.Hkv * p.groups;
+    if (w.x >= w.before + here) {
+      w.before += here;
+      ++w.b;
+      continue;
+    }
+    const int64_t local = w.x - w.before;
+    const int64_t u = local / per;
+    part.b = w.b;
+    part.grp = (int)(u % p.groups);
+    part.kvh = (int)(u / p.groups);
+    part.q0 = (int)(local % per);
+    part.q1 = (int)(per - part.q0 < w.x_end - w.x ? per : part.q0 + (w.x_end - w.x));
+    part.alone = part.q0 == 0 && part.q1 == per;
+    part.unit = (int64_t)w.b * p.c.Hkv * p.groups + u;
+    part.head_row = ((int64_t)w.b * p.c.Hkv + part.kvh) * p.c.capacity;
+    w.x += part.q1 - part.q0;
+    return true;
+  }
+  return false;
 }
 
 // Row of out and lse ([B, Hq, T]) of unit row r (t * rep + head of the group).
 __device__ __forceinline__ int64_t out_row(const Params& p, int b, int kvh, int r) {
   return ((int64_t)b * p.Hq + kvh * p.rep + r % p.rep) * p.T + r / p.rep;
 }
+
+// The launches of tree_tiles.cu and of the merge (tree_rows.cu).
+int launch_tiles(const Params& p, cudaStream_t stream);
 
 }  // namespace tree
 }  // namespace ringattn

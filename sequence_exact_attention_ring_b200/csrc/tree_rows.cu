@@ -521,53 +521,20 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
   using W = Warp<FMT, D, NT>;
   constexpr int kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t s_anc[kMaxNodes], s_vis[kMaxNodes];
-  __shared__ int s_depth[kMaxNodes], s_jump[kMaxNodes];
-  __shared__ int64_t s_plan[4];
+  __shared__ Walk s_walk;
   __shared__ float s_ml[kWarps][kRows][3];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
 
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = RING_ATTN_OK;  // the merge kernel reports
-  if (warp == 0) {
-    int64_t total, before = 0, none;
-    warp_totals(p, 0, total, none);
-    const int64_t act = active_ctas(p, total);
-    const int64_t cta = blockIdx.x;
-    const int64_t x0 = cta < act ? share_begin(total, act, cta) : 0;
-    const int64_t x1 = cta < act ? share_begin(total, act, cta + 1) : 0;
-    const int b = x0 < x1 ? warp_find_sequence(p, x0, before) : p.c.B;
-    if (lane == 0) {
-      s_plan[0] = x0;
-      s_plan[1] = x1;
-      s_plan[2] = b;
-      s_plan[3] = before;
-    }
-  }
+  if (warp == 0) warp_begin_walk(p, &s_walk);
   __syncthreads();
-  int64_t x = s_plan[0];
-  const int64_t x_end = s_plan[1];
-  int b = (int)s_plan[2];
-  int64_t before = s_plan[3];
-
+  Walk walk = s_walk;
+  Part part;
   uint8_t* ring = smem + warp * F::kStages * F::kStageBytes;
-  bool fresh = true;  // masks of sequence b are still to be made
-  while (x < x_end) {
-    const Keys ks = sequence_keys(p, b);
-    const int64_t per = (ks.steps + p.quad - 1) / p.quad;
-    const int64_t here = per * p.c.Hkv * p.groups;
-    if (x >= before + here) {
-      before += here;
-      ++b;
-      fresh = true;
-      continue;
-    }
-    const int64_t local = x - before;
-    const int64_t u_local = local / per;
-    const int grp = (int)(u_local % p.groups), kvh = (int)(u_local / p.groups);
-    const int q0 = (int)(local % per);
-    const int q1 = (int)(per - q0 < x_end - x ? per : q0 + (x_end - x));
-    const int64_t unit = (int64_t)b * p.c.Hkv * p.groups + u_local;
-    const int64_t head_row = ((int64_t)b * p.c.Hkv + kvh) * p.c.capacity;
+  while (next_part(p, walk, part)) {
+    const Keys& ks = part.ks;
+    const int b = part.b, grp = part.grp, kvh = part.kvh, q0 = part.q0, q1 = part.q1;
+    const int64_t unit = part.unit, head_row = part.head_row;
     const int live_rows = ks.cnt * p.rep;
 
     // this warp's steps: one of every quad (the last quad of a unit may be short of some)
@@ -580,10 +547,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
     };
 #pragma unroll 1
     for (int j = 0; j < F::kStages - 1; ++j) prefetch(j);
-    if (fresh) {
-      tree_masks(p, b, ks, s_anc, s_vis, s_depth, s_jump);
-      fresh = false;
-    }
+    const Nodes nodes = warp_nodes(p, b, ks);
 
     // queries in the score product's order of head dimensions (lane column g: query row g of
     // the tile); fp16 ones times 2^(14 - exponent of the row's largest)
@@ -630,9 +594,9 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
       for (int r = 0; r < 2; ++r) {
         row_scale[i][r] = __shfl_sync(0xffffffffu, own_scale[i], 4 * (2 * c + r));
         const int row = grp * kRows + 8 * i + 2 * c + r;
-        const int t = row < live_rows ? row / p.rep : 0;
-        lo_key[i][r] = p.window > 0 ? ks.n + s_depth[t] - p.window + 1 : 0;
-        vis[i][r] = s_vis[t];
+        int depth;
+        node_of(nodes, row < live_rows ? row / p.rep : 0, vis[i][r], depth);
+        lo_key[i][r] = p.window > 0 ? ks.n + depth - p.window + 1 : 0;
       }
 
     float o[NT][D / 16][4];
@@ -789,7 +753,6 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
               make_float4(o[i][d][r], o[i][d][r + 2], o[i][d + 1][r], o[i][d + 1][r + 2]);
       }
     __syncthreads();
-    const bool alone = q0 == 0 && q1 == per;  // the unit's only part
     const int64_t slot = (int64_t)blockIdx.x + unit;
     {
       constexpr int kTpr = kThreads / kRows, kPer = D / kTpr;  // threads and dimensions per row
@@ -822,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
 #pragma unroll
         for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * inv * up;
         const float lse2 = none ? -INFINITY : M + log2f(L);
-        if (alone) {
+        if (part.alone) {
           const int64_t orow = out_row(p, b, kvh, row);
 #pragma unroll
           for (int e = 0; e < kPer; e += 4)
@@ -839,8 +802,24 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
       }
     }
     __syncthreads();  // s_ml and the O tiles are read before the ring is filled again
-    x += q1 - q0;
   }
+}
+
+// Block 0 of a merge: lengths, counts and parents out of range go to the status word.
+__device__ __forceinline__ void report_bad(const Params& p) {
+  int bad = 0;
+  for (int x = threadIdx.x; x < p.c.B; x += 128) {
+    int n, cnt;
+    if (bad_sequence(p, x, n, cnt)) {
+      bad = 1;
+      continue;
+    }
+    for (int t = 0; p.parents && t < cnt; ++t) {
+      const int par = p.parents[(int64_t)x * p.T + t];
+      if (par < -1 || par >= t) bad = 1;
+    }
+  }
+  if (bad) atomicExch(p.status, RING_ATTN_EINVAL);
 }
 
 // One block per unit and row: the row's partials (in the order of the CTAs that made them)
@@ -871,21 +850,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const Params p) {
       s_plan[1] = before;
     }
   }
-  if (blockIdx.x == 0) {
-    int bad = 0;
-    for (int x = threadIdx.x; x < p.c.B; x += 128) {
-      int n, cnt;
-      if (bad_sequence(p, x, n, cnt)) {
-        bad = 1;
-        continue;
-      }
-      for (int t = 0; p.parents && t < cnt; ++t) {
-        const int par = p.parents[(int64_t)x * p.T + t];
-        if (par < -1 || par >= t) bad = 1;
-      }
-    }
-    if (bad) atomicExch(p.status, RING_ATTN_EINVAL);
-  }
+  if (blockIdx.x == 0) report_bad(p);
   __syncthreads();
   if (row >= rows) return;
   const Keys ks = sequence_keys(p, b);
@@ -946,6 +911,60 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const Params p) {
   if (d4 == 0) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(tot)) * 0.69314718055994530942f;
 }
 
+// The same for units of many rows, whose parts are few: one warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) tree_merge_rows_kernel(const Params p) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (blockIdx.x == 0) report_bad(p);
+  const int per_unit = p.rows_per_group / 4;
+  const int64_t ub = (int64_t)p.c.Hkv * p.groups;
+  const int64_t unit = blockIdx.x / per_unit;
+  const int r = (int)(blockIdx.x % per_unit) * 4 + warp;
+  const int b = (int)(unit / ub);
+  const int64_t u_local = unit % ub;
+  const int kvh = (int)(u_local / p.groups);
+  const int row = (int)(u_local % p.groups) * p.rows_per_group + r;
+  if (row >= p.T * p.rep) return;
+  const Keys ks = sequence_keys(p, b);
+  const int64_t per = (ks.steps + p.quad - 1) / p.quad;
+  const int64_t orow = out_row(p, b, kvh, row);
+  constexpr int kPer = D / 32;  // dimensions per lane
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer);
+  if (row >= ks.cnt * p.rep || per == 0) {
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) dst[e] = 0u;
+    if (lane == 0) p.lse[orow] = -INFINITY;
+    return;
+  }
+  int64_t total, before;
+  warp_totals(p, b, total, before);
+  const int64_t act = active_ctas(p, total);
+  const int64_t first = before + u_local * per;
+  const int64_t c0 = share_of(total, act, first), c1 = share_of(total, act, first + per - 1);
+  if (c0 == c1) return;
+  const float* lse = p.lse_parts + (c0 + unit) * p.rows_per_group + r;
+  const float* src = p.o_parts + ((c0 + unit) * p.rows_per_group + r) * D + lane * kPer;
+  const int parts = (int)(c1 - c0 + 1);
+  float M = -INFINITY;
+  for (int i = 0; i < parts; ++i) M = fmaxf(M, lse[(int64_t)i * p.rows_per_group]);
+  float sum = 0.f, acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  if (M != -INFINITY) {
+    for (int i = 0; i < parts; ++i) {
+      const float w = exp2f(lse[(int64_t)i * p.rows_per_group] - M);
+      if (w == 0.f) continue;  // nothing of this part's (possibly empty) row
+      sum += w;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, src[(int64_t)i * p.rows_per_group * D + e], acc[e]);
+    }
+  }
+  const float inv = M == -INFINITY ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < kPer / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if (lane == 0) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * 0.69314718055994530942f;
+}
+
 template <int FMT, int D, int NT>
 int launch_rows_t(const Params& p, cudaStream_t stream) {
   constexpr int smem = Fmt<FMT, D>::smem(8 * NT);
@@ -978,14 +997,25 @@ struct TreePlan {
   int64_t units, slots;
 };
 
+// More than 16 query rows per kv head go to the tcgen05 form, whose tile is 128 rows whatever
+// part of them is real; up to 16 the warp form.
 TreePlan tree_plan(const CacheView& c, int Hq, int T) {
   TreePlan t;
-  t.rows_per_group = T * (Hq / c.Hkv) <= 8 ? 8 : 16;
-  t.groups = (T * (Hq / c.Hkv) + t.rows_per_group - 1) / t.rows_per_group;
-  t.step = tree::step_keys(c.format, c.D);
-  t.quad = tree::kWarps;
-  t.ctas = 148 * (c.D == 128 && t.rows_per_group == 16 ? 2 : 3);
-  t.min_quads = 2;
+  const int rows = T * (Hq / c.Hkv);
+  if (rows > 16) {
+    t.rows_per_group = 128;
+    t.step = 128;
+    t.quad = 1;
+    t.ctas = 148;
+    t.min_quads = 1;
+  } else {
+    t.rows_per_group = rows <= 8 ? 8 : 16;
+    t.step = tree::step_keys(c.format, c.D);
+    t.quad = tree::kWarps;
+    t.ctas = 148 * (c.D == 128 && t.rows_per_group == 16 ? 2 : 3);
+    t.min_quads = 2;
+  }
+  t.groups = (rows + t.rows_per_group - 1) / t.rows_per_group;
   t.units = (int64_t)c.B * c.Hkv * t.groups;
   t.slots = t.ctas + t.units;
   return t;
@@ -1031,17 +1061,29 @@ int launch_tree(const CacheView& c, const void* q, const int64_t* qs, void* out,
   p.watchdog_ns = watchdog_ns;
   if (t.units * t.rows_per_group > 0x7fffffff) return RING_ATTN_EINVAL;
   int rc;
-  switch (c.format) {
-    case RING_ATTN_CACHE_BF16: rc = tree::launch_rows_d<RING_ATTN_CACHE_BF16>(p, stream); break;
-    case RING_ATTN_CACHE_MXFP8: rc = tree::launch_rows_d<RING_ATTN_CACHE_MXFP8>(p, stream); break;
-    default: rc = tree::launch_rows_d<RING_ATTN_CACHE_MXFP4>(p, stream); break;
+  if (t.rows_per_group == 128) {
+    rc = tree::launch_tiles(p, stream);
+  } else {
+    switch (c.format) {
+      case RING_ATTN_CACHE_BF16: rc = tree::launch_rows_d<RING_ATTN_CACHE_BF16>(p, stream); break;
+      case RING_ATTN_CACHE_MXFP8: rc = tree::launch_rows_d<RING_ATTN_CACHE_MXFP8>(p, stream); break;
+      default: rc = tree::launch_rows_d<RING_ATTN_CACHE_MXFP4>(p, stream); break;
+    }
   }
   if (rc) return rc;
-  const unsigned blocks = (unsigned)(t.units * t.rows_per_group);
-  if (c.D == 64)
-    tree::tree_merge_kernel<64><<<blocks, 128, 0, stream>>>(p);
-  else
-    tree::tree_merge_kernel<128><<<blocks, 128, 0, stream>>>(p);
+  if (t.rows_per_group == 128) {
+    const unsigned blocks = (unsigned)(t.units * (t.rows_per_group / 4));
+    if (c.D == 64)
+      tree::tree_merge_rows_kernel<64><<<blocks, 128, 0, stream>>>(p);
+    else
+      tree::tree_merge_rows_kernel<128><<<blocks, 128, 0, stream>>>(p);
+  } else {
+    const unsigned blocks = (unsigned)(t.units * t.rows_per_group);
+    if (c.D == 64)
+      tree::tree_merge_kernel<64><<<blocks, 128, 0, stream>>>(p);
+    else
+      tree::tree_merge_kernel<128><<<blocks, 128, 0, stream>>>(p);
+  }
   return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
 }
 
