@@ -15,6 +15,11 @@
 // multiple of `quad` steps), whatever the lengths are: a CTA's share may end one unit and
 // begin the next. CTA c's part of unit u goes to partial slot c + u, which is unique
 // because every boundary raises one of the two.
+//
+// All of this is 32-bit arithmetic with power-of-two steps, and the parts that run once per
+// unit are functions of their own: these kernels are short, and the instructions that a
+// launch has to fetch first are a good part of its time (with 64-bit divisions inlined the
+// merge alone was 45 KB of code and took 12 us).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -29,6 +34,14 @@ namespace tree {
 
 constexpr int kMaxNodes = 64;
 
+// Functions that run once per unit: calls, except in kernels that move registers between
+// warpgroups (setmaxnreg), which cannot call functions.
+#ifdef TREE_INLINE
+#define TREE_ONCE __device__ __forceinline__
+#else
+#define TREE_ONCE __device__ __noinline__
+#endif
+
 struct Params {
   CacheView c;
   const uint16_t* q;             // bf16, (b, h, t) strides in elements, unit head-dim stride
@@ -42,7 +55,8 @@ struct Params {
   int window, sinks;             // window 0: every committed token
   int groups;                    // row groups per kv head
   int rows_per_group;
-  int step, quad;                // keys per step, steps per unit of division
+  int step, step_log2;           // keys per step
+  int quad_log2;                 // steps per quad, the grain of division
   int ctas;                      // CTAs that share the steps
   int min_quads;                 // least share of a CTA
   float scale_log2;
@@ -63,7 +77,8 @@ struct Keys {
 __device__ __forceinline__ bool bad_sequence(const Params& p, int b, int& n, int& cnt) {
   n = p.lengths[b];
   cnt = p.counts ? p.counts[b] : p.T;
-  return n < 0 || cnt < 0 || cnt > p.T || (int64_t)n + cnt > p.c.capacity;
+  // (capacity <= 2^30 and cnt <= 64: the sum cannot pass 2^31 once n is in range)
+  return n < 0 || cnt < 0 || cnt > p.T || n > (int)p.c.capacity || n + cnt > (int)p.c.capacity;
 }
 
 __device__ __forceinline__ Keys sequence_keys(const Params& p, int b) {
@@ -73,12 +88,12 @@ __device__ __forceinline__ Keys sequence_keys(const Params& p, int b) {
   k.first = 0;
   k.steps = 0;
   if (k.cnt == 0) return k;  // no query row
-  const int end = (int)(((int64_t)k.n + k.cnt + p.step - 1) / p.step);
+  const int end = (k.n + k.cnt + p.step - 1) >> p.step_log2;
   if (p.window > 0) {
     const int lo = k.n - p.window + 1;  // the lowest position that a root's window holds
-    const int w0 = lo > 0 ? lo / p.step : 0;
+    const int w0 = lo > 0 ? lo >> p.step_log2 : 0;
     const int s = p.sinks < k.n ? p.sinks : k.n;
-    const int s_steps = (int)(((int64_t)s + p.step - 1) / p.step);
+    const int s_steps = (s + p.step - 1) >> p.step_log2;
     if (w0 > s_steps) {
       k.sink_steps = s_steps;
       k.first = w0;
@@ -89,7 +104,7 @@ __device__ __forceinline__ Keys sequence_keys(const Params& p, int b) {
 }
 
 __device__ __forceinline__ int step_key(const Params& p, const Keys& k, int i) {
-  return (i < k.sink_steps ? i : k.first + i - k.sink_steps) * p.step;
+  return (i < k.sink_steps ? i : k.first + i - k.sink_steps) << p.step_log2;
 }
 
 // Cache row u can be seen by some query row of the sequence. Rows that none sees (behind
@@ -98,51 +113,61 @@ __device__ __forceinline__ bool key_live(const Params& p, const Keys& k, int u) 
   return u < k.n + k.cnt && (p.window <= 0 || u < p.sinks || u > k.n - p.window);
 }
 
-__device__ __forceinline__ int64_t sequence_quads(const Params& p, int b) {
-  const Keys k = sequence_keys(p, b);
-  return (int64_t)((k.steps + p.quad - 1) / p.quad) * p.c.Hkv * p.groups;
+__device__ __forceinline__ uint32_t unit_quads(const Params& p, const Keys& k) {
+  return (uint32_t)(k.steps + (1 << p.quad_log2) - 1) >> p.quad_log2;
+}
+__device__ __forceinline__ uint32_t sequence_quads(const Params& p, int b) {
+  return unit_quads(p, sequence_keys(p, b)) * (uint32_t)(p.c.Hkv * p.groups);
+}
+
+// How the quads are shared: the first `more` of `ctas` CTAs take base + 1, the others base.
+// None gets less than min_quads (except where there is less in all).
+struct Shares {
+  uint32_t ctas, base, more;
+};
+__device__ __forceinline__ Shares shares_of(const Params& p, uint32_t total) {
+  const uint32_t most = (total + p.min_quads - 1) / p.min_quads;
+  Shares s;
+  s.ctas = most < (uint32_t)p.ctas ? most : (uint32_t)p.ctas;
+  s.base = s.ctas ? total / s.ctas : 0;
+  s.more = total - s.base * s.ctas;
+  return s;
+}
+__device__ __forceinline__ uint32_t share_begin(const Shares& s, uint32_t c) {
+  return c >= s.ctas ? s.base * s.ctas + s.more : c * s.base + (c < s.more ? c : s.more);
+}
+// The CTA whose share holds quad x.
+__device__ __forceinline__ uint32_t share_of(const Shares& s, uint32_t x) {
+  const uint32_t wide = s.more * (s.base + 1);
+  return x < wide ? x / (s.base + 1) : s.more + (x - wide) / s.base;
 }
 
 // One warp: the quads of all units, and the quads of the sequences before `b_stop`.
-__device__ __forceinline__ void warp_totals(const Params& p, int b_stop, int64_t& total, int64_t& before) {
+__device__ __forceinline__ void warp_totals(const Params& p, int b_stop, uint32_t& total, uint32_t& before) {
   const int lane = threadIdx.x % 32;
-  int64_t t = 0, f = 0;
+  uint32_t t = 0, f = 0;
+#pragma unroll 1
   for (int b = lane; b < p.c.B; b += 32) {
-    const int64_t x = sequence_quads(p, b);
+    const uint32_t x = sequence_quads(p, b);
     t += x;
     if (b < b_stop) f += x;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    t += __shfl_xor_sync(0xffffffffu, t, o);
-    f += __shfl_xor_sync(0xffffffffu, f, o);
-  }
-  total = t;
-  before = f;
-}
-
-// CTAs that get a share: none gets less than min_quads (except where there is less in all).
-__device__ __forceinline__ int64_t active_ctas(const Params& p, int64_t total) {
-  const int64_t most = (total + p.min_quads - 1) / p.min_quads;
-  return most < p.ctas ? most : p.ctas;
-}
-__device__ __forceinline__ int64_t share_begin(int64_t total, int64_t ctas, int64_t c) { return total * c / ctas; }
-// The CTA whose share holds quad x: the largest c with share_begin(c) <= x.
-__device__ __forceinline__ int64_t share_of(int64_t total, int64_t ctas, int64_t x) {
-  return ((x + 1) * ctas - 1) / total;
+  total = __reduce_add_sync(0xffffffffu, t);
+  before = __reduce_add_sync(0xffffffffu, f);
 }
 
 // One warp: the sequence that holds quad x, and the quads before it.
-__device__ __forceinline__ int warp_find_sequence(const Params& p, int64_t x, int64_t& before) {
+__device__ __forceinline__ int warp_find_sequence(const Params& p, uint32_t x, uint32_t& before) {
   const int lane = threadIdx.x % 32;
   before = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < p.c.B; b0 += 32) {
     const int b = b0 + lane;
-    const int64_t mine = b < p.c.B ? sequence_quads(p, b) : 0;
-    int64_t incl = mine;
+    const uint32_t mine = b < p.c.B ? sequence_quads(p, b) : 0;
+    uint32_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, before + incl > x);
@@ -164,7 +189,7 @@ struct Nodes {
   int depth[2];
 };
 
-__device__ __forceinline__ Nodes warp_nodes(const Params& p, int b, const Keys& k) {
+TREE_ONCE Nodes warp_nodes(const Params& p, int b, const Keys& k) {
   const int lane = threadIdx.x % 32;
   Nodes x;
   int jump[2];
@@ -183,6 +208,7 @@ __device__ __forceinline__ Nodes warp_nodes(const Params& p, int b, const Keys& 
   }
   if (p.parents != nullptr) {
     // pointer doubling: after round i a node's set holds its first 2^i ancestors
+#pragma unroll 1
     for (int r = 1; r < k.cnt; r <<= 1) {
       uint64_t add[2];
       int next[2];
@@ -206,12 +232,13 @@ __device__ __forceinline__ Nodes warp_nodes(const Params& p, int b, const Keys& 
   // ancestors that fell out of a window shorter than the tree is deep
   if (__any_sync(0xffffffffu, p.window > 0 && (p.window <= x.depth[0] || p.window <= x.depth[1]))) {
     const uint64_t anc[2] = {x.seen[0], x.seen[1]};
+#pragma unroll 1
     for (int j = 0; j < k.cnt; ++j) {
       const int d0 = __shfl_sync(0xffffffffu, x.depth[0], j & 31), d1 = __shfl_sync(0xffffffffu, x.depth[1], j & 31);
       const int dj = j < 32 ? d0 : d1;
 #pragma unroll
       for (int s = 0; s < 2; ++s)
-        if ((anc[s] >> j & 1) && dj <= x.depth[s] - p.window && (int64_t)k.n + dj >= p.sinks)
+        if ((anc[s] >> j & 1) && dj <= x.depth[s] - p.window && k.n + dj >= p.sinks)
           x.seen[s] &= ~(1ull << j);
     }
   }
@@ -232,22 +259,20 @@ struct Part {
   Keys ks;
   int q0, q1;        // quads of the unit
   bool alone;        // the whole unit
-  int64_t unit;
+  int unit;
   int64_t head_row;  // first cache row of (b, kv head)
 };
 struct Walk {
-  int64_t x, x_end, before;  // next quad, end of the share, quads before sequence b
+  uint32_t x, x_end, before;  // next quad, end of the share, quads before sequence b
   int b;
 };
 
 // Called by one warp; `out` (shared memory) then holds the walk for every thread of the CTA.
-__device__ __forceinline__ void warp_begin_walk(const Params& p, Walk* out) {
-  int64_t total, before = 0, none;
+TREE_ONCE void warp_begin_walk(const Params& p, Walk* out) {
+  uint32_t total, before = 0, none;
   warp_totals(p, 0, total, none);
-  const int64_t act = active_ctas(p, total);
-  const int64_t cta = blockIdx.x;
-  const int64_t x0 = cta < act ? share_begin(total, act, cta) : 0;
-  const int64_t x1 = cta < act ? share_begin(total, act, cta + 1) : 0;
+  const Shares sh = shares_of(p, total);
+  const uint32_t x0 = share_begin(sh, blockIdx.x), x1 = share_begin(sh, blockIdx.x + 1);
   const int b = x0 < x1 ? warp_find_sequence(p, x0, before) : p.c.B;
   if (threadIdx.x % 32 == 0) {
     out->x = x0;
@@ -257,30 +282,46 @@ __device__ __forceinline__ void warp_begin_walk(const Params& p, Walk* out) {
   }
 }
 
-__device__ __forceinline__ bool next_part(const Params& p, Walk& w, Part& part) {
+TREE_ONCE bool next_part(const Params& p, Walk& w, Part& part) {
   while (w.x < w.x_end) {
     part.ks = sequence_keys(p, w.b);
-    const int64_t per = (part.ks.steps + p.quad - 1) / p.quad;
-    const int64_t here = per * p.c.Hkv * p.groups;
+    const uint32_t per = unit_quads(p, part.ks);
+    const uint32_t here = per * (uint32_t)(p.c.Hkv * p.groups);
     if (w.x >= w.before + here) {
       w.before += here;
       ++w.b;
       continue;
     }
-    const int64_t local = w.x - w.before;
-    const int64_t u = local / per;
+    const uint32_t local = w.x - w.before;
+    const uint32_t u = local / per;
     part.b = w.b;
-    part.grp = (int)(u % p.groups);
-    part.kvh = (int)(u / p.groups);
-    part.q0 = (int)(local % per);
+    part.kvh = (int)(u / (uint32_t)p.groups);
+    part.grp = (int)u - part.kvh * p.groups;
+    part.q0 = (int)(local - u * per);
     part.q1 = (int)(per - part.q0 < w.x_end - w.x ? per : part.q0 + (w.x_end - w.x));
-    part.alone = part.q0 == 0 && part.q1 == per;
-    part.unit = (int64_t)w.b * p.c.Hkv * p.groups + u;
+    part.alone = part.q0 == 0 && part.q1 == (int)per;
+    part.unit = w.b * p.c.Hkv * p.groups + (int)u;
     part.head_row = ((int64_t)w.b * p.c.Hkv + part.kvh) * p.c.capacity;
     w.x += part.q1 - part.q0;
     return true;
   }
   return false;
+}
+
+// Where a unit's partial results are: those of CTAs first .. first + count - 1, in slots
+// first + unit and following. count 1: the unit was done by one CTA, which wrote the result.
+struct Parts {
+  uint32_t first, count;
+};
+__device__ __forceinline__ Parts warp_parts(const Params& p, int b, uint32_t u_local, uint32_t per) {
+  uint32_t total, before;
+  warp_totals(p, b, total, before);
+  const Shares sh = shares_of(p, total);
+  const uint32_t x = before + u_local * per;
+  Parts r;
+  r.first = share_of(sh, x);
+  r.count = share_of(sh, x + per - 1) - r.first + 1;
+  return r;
 }
 
 // Row of out and lse ([B, Hq, T]) of unit row r (t * rep + head of the group).

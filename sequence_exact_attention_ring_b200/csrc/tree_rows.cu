@@ -50,6 +50,7 @@ namespace tree {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
+static_assert(kWarps == 4, "a quad of steps is one step for each warp");
 constexpr int kLiftP = 13;   // log2 of the factor that p carries into fp16 (see above)
 constexpr int kSpread = 15;  // scales of a step may lie 2^kSpread apart in the fp16 form
 constexpr int kBelow = 3;    // and R this far below E
@@ -516,7 +517,7 @@ struct Warp {
 };
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_kernel(const __grid_constant__ Params p) {
   using F = Fmt<FMT, D>;
   using W = Warp<FMT, D, NT>;
   constexpr int kRows = 8 * NT;
@@ -534,12 +535,12 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
   while (next_part(p, walk, part)) {
     const Keys& ks = part.ks;
     const int b = part.b, grp = part.grp, kvh = part.kvh, q0 = part.q0, q1 = part.q1;
-    const int64_t unit = part.unit, head_row = part.head_row;
+    const int64_t head_row = part.head_row;
     const int live_rows = ks.cnt * p.rep;
 
     // this warp's steps: one of every quad (the last quad of a unit may be short of some)
     const int quads = q1 - q0;
-    auto step_of = [&](int j) { return p.quad * (q0 + j) + warp; };
+    auto step_of = [&](int j) { return kWarps * (q0 + j) + warp; };
     auto prefetch = [&](int j) {
       if (j < quads && step_of(j) < ks.steps)
         W::load(p, ks, head_row, step_key(p, ks, step_of(j)), ring + (j % F::kStages) * F::kStageBytes);
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
         // every row sees all keys of the step
         const bool whole =
             kb + F::kStep <= ks.n &&
-            (p.window <= 0 || kb + F::kStep <= p.sinks || (int64_t)kb >= (int64_t)ks.n + p.T - p.window);
+            (p.window <= 0 || kb + F::kStep <= p.sinks || kb >= ks.n + p.T - p.window);
         uint32_t live = 0xffffffffu;
         int ref[2] = {0, 0};
         bool half = true;
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
               make_float4(o[i][d][r], o[i][d][r + 2], o[i][d + 1][r], o[i][d + 1][r + 2]);
       }
     __syncthreads();
-    const int64_t slot = (int64_t)blockIdx.x + unit;
+    const int64_t slot = (int64_t)blockIdx.x + part.unit;
     {
       constexpr int kTpr = kThreads / kRows, kPer = D / kTpr;  // threads and dimensions per row
       const int r = threadIdx.x / kTpr, d0 = (threadIdx.x % kTpr) * kPer;
@@ -806,16 +807,16 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
 }
 
 // Block 0 of a merge: lengths, counts and parents out of range go to the status word.
-__device__ __forceinline__ void report_bad(const Params& p) {
+__device__ __noinline__ void report_bad(const Params& p) {
   int bad = 0;
-  for (int x = threadIdx.x; x < p.c.B; x += 128) {
+#pragma unroll 1
+  for (int i = threadIdx.x; i < p.c.B * p.T; i += 128) {
+    const int x = i / p.T, t = i - x * p.T;
     int n, cnt;
     if (bad_sequence(p, x, n, cnt)) {
       bad = 1;
-      continue;
-    }
-    for (int t = 0; p.parents && t < cnt; ++t) {
-      const int par = p.parents[(int64_t)x * p.T + t];
+    } else if (p.parents && t < cnt) {
+      const int par = p.parents[i];
       if (par < -1 || par >= t) bad = 1;
     }
   }
@@ -827,50 +828,42 @@ __device__ __forceinline__ void report_bad(const Params& p) {
 // get out = 0 and lse = -inf. A unit that one CTA did alone is only completed by its dead
 // rows. Block 0 writes the status word.
 template <int D>
-__global__ void __launch_bounds__(128) tree_merge_kernel(const Params p) {
+__global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__ Params p) {
   constexpr int kTpr = D / 4;              // threads per partial row (float4 each)
   constexpr int kPar = 128 / kTpr;         // partials in flight
-  __shared__ int64_t s_plan[2];
+  __shared__ Parts s_parts;
   __shared__ float s_max[4];
   __shared__ float s_sum[kPar];
   __shared__ float4 s_acc[kPar][kTpr];
-  const int rows = p.T * p.rep;
-  const int64_t ub = (int64_t)p.c.Hkv * p.groups;
-  const int64_t unit = blockIdx.x / p.rows_per_group;
-  const int r = blockIdx.x % p.rows_per_group;
-  const int b = (int)(unit / ub);
-  const int64_t u_local = unit % ub;
-  const int kvh = (int)(u_local / p.groups), grp = (int)(u_local % p.groups);
-  const int row = grp * p.rows_per_group + r;
-  if (threadIdx.x < 32) {
-    int64_t total, before;
-    warp_totals(p, b, total, before);
-    if (threadIdx.x == 0) {
-      s_plan[0] = total;
-      s_plan[1] = before;
-    }
-  }
   if (blockIdx.x == 0) report_bad(p);
-  __syncthreads();
-  if (row >= rows) return;
+  const int unit = blockIdx.x / p.rows_per_group;
+  const int r = blockIdx.x - unit * p.rows_per_group;
+  const int head = unit / p.groups, b = head / p.c.Hkv, kvh = head - b * p.c.Hkv;
+  const int row = (unit - head * p.groups) * p.rows_per_group + r;
+  if (row >= p.T * p.rep) return;
   const Keys ks = sequence_keys(p, b);
   const int64_t orow = out_row(p, b, kvh, row);
-  const int64_t per = (ks.steps + p.quad - 1) / p.quad;
-  const int64_t total = s_plan[0];
+  const uint32_t per = unit_quads(p, ks);
   const int d4 = threadIdx.x % kTpr, part = threadIdx.x / kTpr;
   if (row >= ks.cnt * p.rep || per == 0) {
     if (threadIdx.x < D / 8) reinterpret_cast<uint4*>(p.out + orow * D)[threadIdx.x] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) p.lse[orow] = -INFINITY;
     return;
   }
-  const int64_t act = active_ctas(p, total);
-  const int64_t first = s_plan[1] + u_local * per;
-  const int64_t c0 = share_of(total, act, first), c1 = share_of(total, act, first + per - 1);
-  if (c0 == c1) return;
-  const float* lse = p.lse_parts + (c0 + unit) * p.rows_per_group + r;
-  const int parts = (int)(c1 - c0 + 1);
+  if (threadIdx.x < 32) {
+    const Parts x = warp_parts(p, b, unit - b * p.c.Hkv * p.groups, per);
+    if (threadIdx.x == 0) s_parts = x;
+  }
+  __syncthreads();
+  const int parts = (int)s_parts.count;
+  if (parts == 1) return;
+  const int64_t slot = (int64_t)s_parts.first + unit;
+  const float* lse = p.lse_parts + slot * p.rows_per_group + r;
+  const float* src = p.o_parts + (slot * p.rows_per_group + r) * D + 4 * d4;
+  const int64_t stride = (int64_t)p.rows_per_group * D;
   float M = -INFINITY;
-  for (int i = threadIdx.x; i < parts; i += 128) M = fmaxf(M, lse[(int64_t)i * p.rows_per_group]);
+#pragma unroll 1
+  for (int i = threadIdx.x; i < parts; i += 128) M = fmaxf(M, lse[i * p.rows_per_group]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = M;
@@ -879,12 +872,11 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const Params p) {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
   if (M != -INFINITY) {
+#pragma unroll 4
     for (int i = part; i < parts; i += kPar) {
-      const float w = exp2f(lse[(int64_t)i * p.rows_per_group] - M);
-      const float4 v = *reinterpret_cast<const float4*>(
-          p.o_parts + ((c0 + unit + i) * p.rows_per_group + r) * D + 4 * d4);
-      if (w == 0.f) continue;  // nothing of this part's (possibly empty) row
-      sum += w;
+      const float w = ex2_approx(lse[i * p.rows_per_group] - M);
+      const float4 v = *reinterpret_cast<const float4*>(src + i * stride);
+      sum += w;  // an empty part's row is 0 and so is its weight
       acc.x = fmaf(w, v.x, acc.x);
       acc.y = fmaf(w, v.y, acc.y);
       acc.z = fmaf(w, v.z, acc.z);
@@ -913,20 +905,17 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const Params p) {
 
 // The same for units of many rows, whose parts are few: one warp per row.
 template <int D>
-__global__ void __launch_bounds__(128) tree_merge_rows_kernel(const Params p) {
+__global__ void __launch_bounds__(128) tree_merge_rows_kernel(const __grid_constant__ Params p) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (blockIdx.x == 0) report_bad(p);
   const int per_unit = p.rows_per_group / 4;
-  const int64_t ub = (int64_t)p.c.Hkv * p.groups;
-  const int64_t unit = blockIdx.x / per_unit;
-  const int r = (int)(blockIdx.x % per_unit) * 4 + warp;
-  const int b = (int)(unit / ub);
-  const int64_t u_local = unit % ub;
-  const int kvh = (int)(u_local / p.groups);
-  const int row = (int)(u_local % p.groups) * p.rows_per_group + r;
+  const int unit = blockIdx.x / per_unit;
+  const int r = (blockIdx.x - unit * per_unit) * 4 + warp;
+  const int head = unit / p.groups, b = head / p.c.Hkv, kvh = head - b * p.c.Hkv;
+  const int row = (unit - head * p.groups) * p.rows_per_group + r;
   if (row >= p.T * p.rep) return;
   const Keys ks = sequence_keys(p, b);
-  const int64_t per = (ks.steps + p.quad - 1) / p.quad;
+  const uint32_t per = unit_quads(p, ks);
   const int64_t orow = out_row(p, b, kvh, row);
   constexpr int kPer = D / 32;  // dimensions per lane
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer);
@@ -936,27 +925,41 @@ __global__ void __launch_bounds__(128) tree_merge_rows_kernel(const Params p) {
     if (lane == 0) p.lse[orow] = -INFINITY;
     return;
   }
-  int64_t total, before;
-  warp_totals(p, b, total, before);
-  const int64_t act = active_ctas(p, total);
-  const int64_t first = before + u_local * per;
-  const int64_t c0 = share_of(total, act, first), c1 = share_of(total, act, first + per - 1);
-  if (c0 == c1) return;
-  const float* lse = p.lse_parts + (c0 + unit) * p.rows_per_group + r;
-  const float* src = p.o_parts + ((c0 + unit) * p.rows_per_group + r) * D + lane * kPer;
-  const int parts = (int)(c1 - c0 + 1);
+  const Parts x = warp_parts(p, b, unit - b * p.c.Hkv * p.groups, per);
+  const int parts = (int)x.count;
+  if (parts == 1) return;
+  const int64_t slot = (int64_t)x.first + unit;
+  const float* lse = p.lse_parts + slot * p.rows_per_group + r;
+  const float* src = p.o_parts + (slot * p.rows_per_group + r) * D + lane * kPer;
   float M = -INFINITY;
-  for (int i = 0; i < parts; ++i) M = fmaxf(M, lse[(int64_t)i * p.rows_per_group]);
+#pragma unroll 1
+  for (int i = lane; i < parts; i += 32) M = fmaxf(M, lse[(int64_t)i * p.rows_per_group]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float sum = 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
   if (M != -INFINITY) {
-    for (int i = 0; i < parts; ++i) {
-      const float w = exp2f(lse[(int64_t)i * p.rows_per_group] - M);
-      if (w == 0.f) continue;  // nothing of this part's (possibly empty) row
-      sum += w;
+    // lane i holds the weight of part i0 + i; the loads of the parts' rows do not wait for it
+#pragma unroll 1
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      const float mine = i0 + lane < parts ? ex2_approx(lse[(int64_t)(i0 + lane) * p.rows_per_group] - M) : 0.f;
+      const int n = min(32, parts - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float w = __shfl_sync(0xffffffffu, mine, i);
+        const float* row_at = src + (int64_t)(i0 + i) * p.rows_per_group * D;
+        float v[kPer];
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, src[(int64_t)i * p.rows_per_group * D + e], acc[e]);
+        for (int e = 0; e < kPer; e += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(row_at + e);
+          v[e] = x.x;
+          v[e + 1] = x.y;
+        }
+        sum += w;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, v[e], acc[e]);  // an empty part's row is 0 and so is w
+      }
     }
   }
   const float inv = M == -INFINITY ? 0.f : 1.f / sum;
@@ -993,7 +996,7 @@ namespace {
 
 // Shape of a launch: row groups, the division's grain and the partial slots.
 struct TreePlan {
-  int rows_per_group, groups, step, quad, ctas, min_quads;
+  int rows_per_group, groups, step, quad_log2, ctas, min_quads;
   int64_t units, slots;
 };
 
@@ -1005,13 +1008,13 @@ TreePlan tree_plan(const CacheView& c, int Hq, int T) {
   if (rows > 16) {
     t.rows_per_group = 128;
     t.step = 128;
-    t.quad = 1;
+    t.quad_log2 = 0;
     t.ctas = 148;
     t.min_quads = 1;
   } else {
     t.rows_per_group = rows <= 8 ? 8 : 16;
     t.step = tree::step_keys(c.format, c.D);
-    t.quad = tree::kWarps;
+    t.quad_log2 = 2;
     t.ctas = 148 * (c.D == 128 && t.rows_per_group == 16 ? 2 : 3);
     t.min_quads = 2;
   }
@@ -1051,7 +1054,8 @@ int launch_tree(const CacheView& c, const void* q, const int64_t* qs, void* out,
   p.groups = t.groups;
   p.rows_per_group = t.rows_per_group;
   p.step = t.step;
-  p.quad = t.quad;
+  p.step_log2 = t.step == 128 ? 7 : (t.step == 32 ? 5 : 4);
+  p.quad_log2 = t.quad_log2;
   p.ctas = t.ctas;
   p.min_quads = t.min_quads;
   p.scale_log2 = scale * 1.4426950408889634f;
@@ -1059,7 +1063,10 @@ int launch_tree(const CacheView& c, const void* q, const int64_t* qs, void* out,
   p.lse_parts = p.o_parts + (size_t)t.slots * t.rows_per_group * c.D;
   p.status = static_cast<int*>(workspace);
   p.watchdog_ns = watchdog_ns;
-  if (t.units * t.rows_per_group > 0x7fffffff) return RING_ATTN_EINVAL;
+  // the device's arithmetic on units and their quads is in 32 bits
+  const int64_t quads = t.units * ((c.capacity / t.step + 2) / (1 << t.quad_log2) + 1);
+  if (t.units * t.rows_per_group > 0x7fffffff || quads > 0x7fffffff || (int64_t)c.B * T > 0x7fffffff)
+    return RING_ATTN_EINVAL;
   int rc;
   if (t.rows_per_group == 128) {
     rc = tree::launch_tiles(p, stream);

@@ -6,30 +6,42 @@
 // rows at a time.
 //
 // What bounds it: the tensor cores (4 * 128 * 128 * D flops per tile of 128 rows, whatever
-// part of the group's rows is real) once a cache row is used by more rows than its bytes pay
-// for; before that the conversion of codes, 2.3 instructions per element on 7 warps. The
-// cache's rows come in as they are (each converting thread copies and later reads its own 16
-// bytes, so the ring of raw tiles needs no barrier), are converted to bf16 in registers and
-// written once into the swizzled K and V tiles that the products read. bf16 rows are copied
-// straight into those tiles.
+// part of the group's rows is real), the exponentials (128 x 128 per tile at 16 a clock: as
+// long as the products at D = 128) and, with codes, their conversion. The cache's rows are
+// contiguous and come in as they are, by bulk copies into a ring of raw tiles; eight warps
+// convert them, 8 elements at a time, into the swizzled K and V tiles that the products read.
+// bf16 rows are copied straight into those tiles.
 //
-// Roles (512 threads): warps 0-7 softmax (warp w: rows 32 (w % 4) .., keys 64 (w / 4) .. of a
-// tile; the two warps of a row agree on its maximum through shared memory), warp 8 issues the
-// products, warps 9-15 fill the tiles. Tensor memory: S double-buffered [0,128) and
-// [128,256), O [256,384), Q [384,448). Every role walks the CTA's share of the work by itself
-// (tree_common.cuh), so tiles of the next unit are filled while the last one is finished.
+// Roles (640 threads): warps 0-3 softmax of the even tiles, warps 4-7 of the odd ones (warp w:
+// rows 32 (w % 4) ..), warps 8-11 fill K tiles, warps 12-15 V tiles, warp 16 issues the
+// products, warp 17 fetches raw tiles, warps 18 and 19 look at their scales. A softmax warp first takes
+// its tile's row maxima and hands the row's reference maximum to the warp of the next tile,
+// then exponentiates while that one is already at its maxima: the chain from tile to tile is
+// the short first half only. (With both warps on one tile, 64 columns each, a tile took 5000
+// clocks: every step of the chain waited for the one before.) Tensor memory: S double-buffered
+// [0,128) and [128,256), O [256,384), Q [384,448) and, in bf16, [448,512). Every role walks
+// the CTA's share of the work by itself (tree_common.cuh), so tiles of the next unit are
+// filled while the last one is finished.
 //
-// Codes to bf16: the bits of tree_rows.cu's bf16 form, one multiplication. To keep its factor
-// inside bf16's range, K and V are held 2^40 too small and Q and P 2^40 too large (exact);
-// blocks whose scale byte is above 160 take two multiplications. Elements are written in the
-// order that the bit operations give (4 codes: 0 2 1 3, 8 codes: 0 4 1 5 2 6 3 7); Q is
-// stored in the same order and the output put back.
+// Codes become fp16 operands as in tree_rows.cu, two per conversion instruction, times their
+// block's scale and 2^6 (e4m3) or 2^8 (e2m1): fp16 then holds every value of a block exactly
+// when its scale 2^k has -20 <= k <= 1 or -22 <= k <= 5 (largest magnitudes of 2^-12 to 896, or
+// 2^-20 to 192). The weights p = 2^(s - m) <= 2^6 enter as p 2^9, so that fp16 rounds them to
+// 11 bits down to 2^-23 and below that by at most 2^-34; a query row with its largest element
+// in [2^14, 2^15). A K or V tile with a scale outside that range is converted to bf16 instead,
+// and its product taken with the bf16 form of Q or P: the code's sign, exponent and mantissa
+// bits are moved to bf16's (times 2^-120 or 2^-126 of the value), and two exact
+// multiplications bring in the rest.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "sm100_ptx.cuh"
 #include "softmax_rows.cuh"
+#define TREE_INLINE
 #include "tree_common.cuh"
 
 namespace ringattn {
@@ -38,48 +50,72 @@ namespace tiles {
 
 constexpr int TK = 128;   // cache rows per tile
 constexpr int TM = 128;   // query rows per group
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kMmaWarp = 8;
-constexpr int kFillWarp = 9;  // first of the filling warps
-constexpr int kFillWarps = 7;
+constexpr int kFillWarp = 8;  // four warps for K, four for V
+constexpr int kFillWarps = 4;
 constexpr int kFill = 32 * kFillWarps;
+constexpr int kMmaWarp = 16;
+constexpr int kFetchWarp = 17;
+constexpr int kScaleWarp = 18;  // two: K's and V's scales
+constexpr int kLaunchRegs = 96;  // 65536 / 640, rounded down to a multiple of 8
+constexpr int kRegsSoftmax = 144, kRegsFill = 72, kRegsOther = 48;
+static_assert(2 * kRegsSoftmax + 2 * kRegsFill + kRegsOther <= 5 * kLaunchRegs, "register split exceeds the launch pool");
 constexpr int kBoxBytes = TK * 128;  // 128 rows x 64 elements
 constexpr int kSmemLimit = 232448;
-constexpr uint32_t kTmemCols = 512, kColO = 256, kColQ = 384;
-constexpr float kRescale = 8.f;
+constexpr uint32_t kTmemCols = 512, kColO = 256, kColQ = 384, kColQb = 448;
+constexpr int kMaxRaw = 4;
+constexpr int kFlags = 16;  // tiles whose form is remembered (more than are ever in flight)
+
+enum Bar { kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kSFull = 8, kPReady = 10, kPvDone = 12, kQReady = 13,
+           kODone = 14, kDrain = 15, kPair = 16, kMax = 20, kRawFull = 28, kRawFree = kRawFull + kMaxRaw,
+           kRawSeen = kRawFree + kMaxRaw, kNumBars = kRawSeen + 2 * kMaxRaw };
 
 template <int FMT, int D>
 struct Cfg {
   static constexpr bool kMx = FMT != RING_ATTN_CACHE_BF16;
   static constexpr int kRowBytes = cache_row_bytes<FMT>(D);
   static constexpr int kChunks = kRowBytes / 16;       // per row
-  static constexpr int kTileChunks = TK * kChunks;
-  static constexpr int kPer = (kTileChunks + kFill - 1) / kFill;  // chunks per filling thread and tile
+  static constexpr int kTileChunks = TK * kChunks;     // 16-byte chunks of a tile of bf16 rows
   static constexpr int kTileBytes = TK * D * 2;        // a bf16 tile
   static constexpr int kOffV = 2 * kTileBytes;
   static constexpr int kOffRaw = 4 * kTileBytes;
-  static constexpr int kRawBytes = kMx ? 2 * kPer * kFill * 20 : 0;  // codes and scale words of K and V
+  // a raw tile: K codes, V codes, K scales, V scales
+  static constexpr int kScaleRow = kMx ? D / kMxBlock : 0;
+  static constexpr int kRawScale = 2 * TK * kRowBytes;
+  static constexpr int kRawBytes = 2 * TK * (kRowBytes + kScaleRow);
   static constexpr int kRawFit = kMx ? (kSmemLimit - 1024 - 2048 - kOffRaw - 512) / kRawBytes : 0;
-  static constexpr int kRaw = kRawFit < 4 ? kRawFit : 4;
+  static constexpr int kRaw = kRawFit < kMaxRaw ? kRawFit : kMaxRaw;
   static_assert(!kMx || kRaw >= 2, "a tile is fetched while another is converted");
+  // Converting: a task is 16 elements of one row, two 16-byte chunks out. Four lanes take the
+  // four tasks of a 64-element box, the next four those of the next row: their 8 stores of one
+  // instruction fall on different chunk positions, as the swizzle of neighbouring rows differs
+  // in the lowest bit. A thread's rows lie a multiple of 8 apart, so its positions stay.
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kRowStep = kFill / (4 * kBoxes);
+  static constexpr int kPasses = TK / kRowStep;
+  static_assert(kRowStep % 8 == 0 && TK % kRowStep == 0, "one swizzled position per thread");
   static constexpr int kOffMax = kOffRaw + kRaw * kRawBytes;  // [2][2][128] floats
   static constexpr int kOffBar = kOffMax + 2048;
-  static constexpr int kSmemBytes = kOffBar + 256 + 1024;
+  static constexpr int kSmemBytes = kOffBar + 512 + 1024;  // barriers, flags, alignment
+  static_assert(kNumBars * 8 + 16 + 2 * kFlags <= 512, "barriers and flags");
   static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
-  static constexpr float kLift = kMx ? 40.f : 0.f;
+  // p's factor in the operand, how far a score may pass the reference before it moves, and the
+  // codes' factor
+  static constexpr float kLift = kMx ? 9.f : 0.f;
+  static constexpr float kRescale = kMx ? 6.f : 8.f;
+  static constexpr int kBias = !kMx ? 0 : (FMT == RING_ATTN_CACHE_MXFP8 ? 6 : 8);
+  // smallest and largest scale byte whose blocks fp16 holds exactly with that factor
+  static constexpr uint32_t kLeast = 127 - 14 - kBias;
+  static constexpr uint32_t kMost = 127 + (FMT == RING_ATTN_CACHE_MXFP8 ? 7 : 13) - kBias;
+  static constexpr uint32_t kBf16Types = (1u << 7) | (1u << 10);  // operand types of the instruction descriptor
   static constexpr uint32_t kIdescS = idesc_bf16_f32(TM, TK, 0, 0);
   static constexpr uint32_t kIdescO = idesc_bf16_f32(TM, D, 0, 1);
 };
-enum Bar { kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kSFull = 8, kPReady = 10, kPvDone = 12, kQReady = 13,
-           kODone = 14, kDrain = 15, kPair = 16, kNumBars = 20 };
 
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -91,127 +127,249 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t mul2h(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_pair_f16(uint32_t codes16) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)codes16));
+  return d;
+}
+// The four pairs of a word of e2m1 codes.
+__device__ __forceinline__ void e2m1_pairs_f16(uint32_t w, uint32_t (&v)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(w));
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 <= e <= 127
+
 __device__ __forceinline__ void store16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-__device__ __forceinline__ uint4 load16(uint32_t src) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src));
-  return v;
-}
-__device__ __forceinline__ uint32_t load4(uint32_t src) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(src));
-  return v;
-}
-
 // Bits c of [lo, hi) in 0..31 for a chunk of columns that starts at c0.
 __device__ __forceinline__ uint32_t span_bits(int lo, int hi, int c0) {
   lo = max(lo - c0, 0);
   hi = min(hi - c0, 32);
   return hi <= lo ? 0u : (0xffffffffu >> (32 - (hi - lo))) << lo;
 }
-__device__ __forceinline__ int clip(int64_t x) { return x <= 0 ? 0 : (x >= TK ? TK : (int)x); }
+__device__ __forceinline__ int clip(int x) { return x <= 0 ? 0 : (x >= TK ? TK : x); }
 
-// The CTA's tiles one by one (of all its parts).
+// exp_pack of softmax_rows.cuh, the weights packed to fp16 or bf16.
+__device__ __forceinline__ float exp_pack_as(uint32_t (&sr)[64], float scale_log2, float m_sub, bool half,
+                                             uint32_t (&pk)[32]) {
+  const uint64_t c2 = f2_splat(scale_log2), negm = f2_splat(-m_sub);
+  uint64_t acc[2] = {0, 0};
+#pragma unroll
+  for (int c = 0; c < 64; c += 2) {
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(sr[c], sr[c + 1]), c2, negm), x0, x1);
+    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+    acc[c / 2 % 2] = f2_add(acc[c / 2 % 2], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
+    sr[c] = __float_as_uint(p0);
+    sr[c + 1] = __float_as_uint(p1);
+  }
+  if (half) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) pk[c] = pack_f16x2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
+  } else {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]));
+  }
+  float t0, t1;
+  f2_unpack(f2_add(acc[0], acc[1]), t0, t1);
+  return t0 + t1;
+}
+
+// The CTA's tiles one by one (of all its parts): for (it.start(w); it.next(p);) ...
 struct TileIter {
   Walk walk;
   Part part;
   int i;
-  bool valid;
-  __device__ __forceinline__ void begin(const Params& p, const Walk& w) {
+  __device__ __forceinline__ void start(const Walk& w) {
     walk = w;
-    valid = next_part(p, walk, part);
-    i = valid ? part.q0 : 0;
+    part.q1 = 0;
+    i = -1;
   }
-  __device__ __forceinline__ void next(const Params& p) {
-    if (++i < part.q1) return;
-    valid = next_part(p, walk, part);
-    i = valid ? part.q0 : 0;
+  __device__ __forceinline__ bool next(const Params& p) {
+    if (++i < part.q1) return true;
+    if (!next_part(p, walk, part)) return false;
+    i = part.q0;
+    return true;
   }
 };
+
+// mbar_wait of sm100_ptx.cuh in less code: the whole warp polls; the clock and the abort flag
+// are looked at every 32 polls.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  uint64_t since = 0;
+#pragma unroll 1
+  for (uint32_t n = 0;; ++n) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (n % 32 == 31) {
+      const uint64_t now = global_timer_ns();
+      if (since == 0) since = now;
+      bool stop = watchdog_aborted(wd);
+      if (now - since > wd.limit_ns) {
+        watchdog_trip(wd);
+        stop = true;
+      }
+      if (__any_sync(0xffffffffu, stop)) return false;
+    }
+  }
+}
 
 template <int FMT, int D>
 struct Fill {
   using C = Cfg<FMT, D>;
 
-  // Raw copies of one tile into this thread's ring slot.
-  static __device__ __forceinline__ void fetch(const Params& p, const TileIter& it, uint32_t slot, int ct) {
+  // One thread: the rows of a tile as they are, up to the cache's end (rows past it are dead).
+  static __device__ __forceinline__ void fetch(const Params& p, const TileIter& it, uint8_t* slot, uint64_t* full) {
     const int kb = step_key(p, it.part.ks, it.i);
     const int64_t first = it.part.head_row + kb;
-    constexpr int kScaleRow = D / kMxBlock;
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint8_t* rows = static_cast<const uint8_t*>(kv ? p.c.v : p.c.k) + first * C::kRowBytes;
-      const uint8_t* sc = static_cast<const uint8_t*>(kv ? p.c.v_scale : p.c.k_scale);
-#pragma unroll
-      for (int i = 0; i < C::kPer; ++i) {
-        const int idx = ct + i * kFill;
-        if (idx < C::kTileChunks) {
-          const int row = idx / C::kChunks;
-          const bool live = key_live(p, it.part.ks, kb + row);
-          copy16(slot + ((kv * C::kPer + i) * kFill + ct) * 16, rows + (live ? idx * 16 : 0), live);
-          // the word that holds the row's scale bytes (with D = 64 its pair's too)
-          const int64_t at = ((first + (live ? row : 0)) * kScaleRow) & ~(int64_t)3;
-          copy4(slot + 2 * C::kPer * kFill * 16 + ((kv * C::kPer + i) * kFill + ct) * 4, sc + at, live);
-        }
-      }
-    }
+    const uint32_t rows = (uint32_t)(p.c.capacity - kb < TK ? p.c.capacity - kb : TK);  // a multiple of 16
+    mbar_arrive_expect_tx(full, 2 * rows * (C::kRowBytes + C::kScaleRow));
+    bulk_load(slot, static_cast<const uint8_t*>(p.c.k) + first * C::kRowBytes, rows * C::kRowBytes, full);
+    bulk_load(slot + TK * C::kRowBytes, static_cast<const uint8_t*>(p.c.v) + first * C::kRowBytes, rows * C::kRowBytes,
+              full);
+    uint8_t* sc = slot + C::kRawScale;
+    bulk_load(sc, static_cast<const uint8_t*>(p.c.k_scale) + first * C::kScaleRow, rows * C::kScaleRow, full);
+    bulk_load(sc + TK * C::kScaleRow, static_cast<const uint8_t*>(p.c.v_scale) + first * C::kScaleRow,
+              rows * C::kScaleRow, full);
   }
 
-  // This thread's chunks of K (kv = 0) or V to bf16, into the swizzled tile at `dst`.
-  static __device__ __forceinline__ void convert(uint32_t slot, int kv, uint32_t dst, int ct) {
+  // Rows of a raw tile that lie past the cache's end or that no query row sees hold anything.
+  static __device__ __forceinline__ bool whole(const Params& p, const TileIter& it, int kb) {
+    return kb + TK <= it.part.ks.n + it.part.ks.cnt &&
+           (p.window <= 0 || kb + TK <= p.sinks || kb > it.part.ks.n - p.window);
+  }
+
+  // One warp: whether K's (kv = 0) or V's scales leave fp16's range.
+  static __device__ __forceinline__ bool wide(const Params& p, const TileIter& it, const uint8_t* slot, int kv) {
+    using Word = typename std::conditional<C::kScaleRow == 4, uint32_t, uint16_t>::type;
+    const int lane = threadIdx.x % 32;
+    const int kb = step_key(p, it.part.ks, it.i);
+    const bool all = whole(p, it, kb);
+    const Word* sc = reinterpret_cast<const Word*>(slot + C::kRawScale + kv * TK * C::kScaleRow) + lane;
+    uint32_t top = 0, low = 0x00ff00ffu;
 #pragma unroll
-    for (int i = 0; i < C::kPer; ++i) {
-      const int idx = ct + i * kFill;
-      if (idx >= C::kTileChunks) break;
-      const int row = idx / C::kChunks, ch = idx % C::kChunks;
-      const uint4 w4 = load16(slot + ((kv * C::kPer + i) * kFill + ct) * 16);
-      const uint32_t sw = load4(slot + 2 * C::kPer * kFill * 16 + ((kv * C::kPer + i) * kFill + ct) * 4);
-      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-      const int blk = FMT == RING_ATTN_CACHE_MXFP8 ? ch / 2 : ch;
-      const uint32_t byte = sw >> (8 * (D == 64 ? 2 * (row & 1) + blk : blk)) & 255u;
-      // held value = raw * 2^120 (or 126) * 2^(byte - 127) * 2^-40
-      constexpr int kUp = (FMT == RING_ATTN_CACHE_MXFP8 ? 120 : 126) - 40;
-      const bool far = byte > 160u;
-      uint32_t f = ((far ? byte - 100u : byte) + kUp) << 7;
-      if (byte == 255u) f = 0x7fc0u;
-      f *= 0x10001u;
-      const uint32_t row_at = dst + row * 128;
-      auto put = [&](uint32_t (&v)[4], int c16) {  // 16-byte chunk c16 of the row's D elements
-        if (far) {
+    for (int i = 0; i < TK / 32; ++i) {
+      const uint32_t w = all || key_live(p, it.part.ks, kb + lane + 32 * i) ? sc[32 * i] : 0x7f7f7f7fu;
+      const uint32_t a = w & 0x00ff00ffu, b = w >> 8 & 0x00ff00ffu;
+      if (C::kScaleRow == 4) {
+        top = __vmaxu2(top, __vmaxu2(a, b));
+        low = __vminu2(low, __vminu2(a, b));
+      } else {  // two bytes: one in the low half of a and of b
+        top = max(top, max(a & 255u, b & 255u));
+        low = min(low & 255u, min(a & 255u, b & 255u));
+      }
+    }
+    const uint32_t hi = max(top & 0xffffu, top >> 16);
+    const uint32_t lo = C::kScaleRow == 4 ? min(low & 0xffffu, low >> 16) : low & 255u;
+    return __any_sync(0xffffffffu, hi > C::kMost || lo < C::kLeast) != 0;
+  }
+
+  // K (kv = 0) or V of a raw tile into the swizzled tile at `dst`, in fp16 or (wide) bf16.
+  static __device__ __forceinline__ void convert(const Params& p, const TileIter& it, const uint8_t* slot, int kv,
+                                                 bool wide, uint32_t dst, int ct) {
+    const int kb = step_key(p, it.part.ks, it.i);
+    const int j = ct % 4, box = ct / 8 % C::kBoxes;                       // task of the box; box
+    const int row0 = ct / (8 * C::kBoxes) * 2 + (ct / 4 & 1);
+    constexpr int kWords = FMT == RING_ATTN_CACHE_MXFP8 ? 4 : 2;          // of codes per task
+    const uint8_t* from = slot + kv * TK * C::kRowBytes + row0 * C::kRowBytes + (box * 4 + j) * 4 * kWords;
+    const uint8_t* sc = slot + C::kRawScale + kv * TK * C::kScaleRow + row0 * C::kScaleRow + box * 2 + j / 2;
+    const uint32_t to0 = dst + box * kBoxBytes + row0 * 128 + (((2 * j) ^ (row0 & 7)) * 16);
+    const uint32_t to1 = dst + box * kBoxBytes + row0 * 128 + (((2 * j + 1) ^ (row0 & 7)) * 16);
+    const bool all = whole(p, it, kb);
+    // the loads of a batch of passes before its first store: loads may not pass the stores
+    constexpr int kBatch = C::kPasses < 4 ? C::kPasses : 4;
+#pragma unroll 1
+    for (int i0 = 0; i0 < C::kPasses; i0 += kBatch) {
+      uint32_t words[kBatch][kWords], bytes[kBatch];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) v[x] = mul2(v[x], 0x71807180u);  // 2^100
+      for (int i = 0; i < kBatch; ++i) {
+        const int row = (i0 + i) * C::kRowStep;
+        bytes[i] = sc[row * C::kScaleRow];
+        if constexpr (FMT == RING_ATTN_CACHE_MXFP8) {
+          const uint4 x = *reinterpret_cast<const uint4*>(from + row * C::kRowBytes);
+          words[i][0] = x.x; words[i][1] = x.y; words[i][2] = x.z; words[i][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(from + row * C::kRowBytes);
+          words[i][0] = x.x; words[i][1] = x.y;
         }
-        store16(row_at + (c16 / 8) * kBoxBytes + (((c16 % 8) ^ (row & 7)) * 16), v[0], v[1], v[2], v[3]);
-      };
-      if constexpr (FMT == RING_ATTN_CACHE_MXFP8) {
-        // lanes of the row's two halves write their two chunks in opposite order (bank conflicts)
-        const int flip = ch / 4 & 1;
+        if (__builtin_expect(!all, 0) && !key_live(p, it.part.ks, kb + row0 + row)) {
+          bytes[i] = 127u;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int y = x ^ flip;
-          const uint32_t a = y ? w[2] : w[0], b = y ? w[3] : w[1];
-          const uint32_t a8 = a << 8, b8 = b << 8;
-          uint32_t v[4] = {mul2(((a8 >> 4) & 0x07f007f0u) | (a8 & 0x80008000u), f),
-                           mul2(((a >> 4) & 0x07f007f0u) | (a & 0x80008000u), f),
-                           mul2(((b8 >> 4) & 0x07f007f0u) | (b8 & 0x80008000u), f),
-                           mul2(((b >> 4) & 0x07f007f0u) | (b & 0x80008000u), f)};
-          put(v, 2 * ch + y);
+          for (int x = 0; x < kWords; ++x) words[i][x] = 0u;
+        }
+      }
+      const uint32_t off = i0 * C::kRowStep * 128;
+      if (__builtin_expect(!wide, 1)) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          // 2^(byte - 127 + kBias) in both halves, fields (byte - 112 + kBias) << 10
+          const uint32_t f = bytes[i] * 0x4000400u + (uint32_t)(C::kBias - 112) * 0x4000400u;
+          uint32_t v[8];
+          if constexpr (FMT == RING_ATTN_CACHE_MXFP8) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] = e4m3_pair_f16(words[i][x / 2] >> (16 * (x % 2)));
+          } else {
+            uint32_t a[4], b[4];
+            e2m1_pairs_f16(words[i][0], a);
+            e2m1_pairs_f16(words[i][1], b);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              v[x] = a[x];
+              v[4 + x] = b[x];
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[x] = mul2h(v[x], f);
+          store16(to0 + off + i * C::kRowStep * 128, v[0], v[1], v[2], v[3]);
+          store16(to1 + off + i * C::kRowStep * 128, v[4], v[5], v[6], v[7]);
         }
       } else {
-        // chunk ch: elements 32 ch .., one output chunk per word
-        const int flip = ch >> 1 << 1;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int y = x ^ flip;
-          const uint32_t a = y == 0 ? w[0] : (y == 1 ? w[1] : (y == 2 ? w[2] : w[3]));
-          const uint32_t a0 = a << 12, a1 = a << 8, a2 = a << 4;
-          uint32_t v[4] = {mul2(((a0 >> 6) & 0x01c001c0u) | (a0 & 0x80008000u), f),
-                           mul2(((a1 >> 6) & 0x01c001c0u) | (a1 & 0x80008000u), f),
-                           mul2(((a2 >> 6) & 0x01c001c0u) | (a2 & 0x80008000u), f),
-                           mul2(((a >> 6) & 0x01c001c0u) | (a & 0x80008000u), f)};
-          put(v, 4 * ch + y);
+        for (int i = 0; i < kBatch; ++i) {
+          // raw * 2^120 (or 126) * 2^(byte - 127 + kBias), as 2^(byte - 127 + 20 or 26 + kBias), 2^100
+          constexpr uint32_t kUp = (FMT == RING_ATTN_CACHE_MXFP8 ? 20 : 26) + C::kBias;
+          const uint32_t e = bytes[i] + kUp;  // the factor's exponent field; past its end (2^93 and more) infinity
+          const uint32_t f = bytes[i] == 255u ? 0x7fc07fc0u : (e < 255u ? e * 0x800080u : 0x7f807f80u);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[4];
+            if constexpr (FMT == RING_ATTN_CACHE_MXFP8) {
+              const uint32_t w0 = h ? words[i][2] : words[i][0], w1 = h ? words[i][3] : words[i][1];
+              const uint32_t e0 = ((w0 << 4) & 0x07f007f0u) | ((w0 << 8) & 0x80008000u);
+              const uint32_t o0 = ((w0 >> 4) & 0x07f007f0u) | (w0 & 0x80008000u);
+              const uint32_t e1 = ((w1 << 4) & 0x07f007f0u) | ((w1 << 8) & 0x80008000u);
+              const uint32_t o1 = ((w1 >> 4) & 0x07f007f0u) | (w1 & 0x80008000u);
+              v[0] = __byte_perm(e0, o0, 0x5410);
+              v[1] = __byte_perm(e0, o0, 0x7632);
+              v[2] = __byte_perm(e1, o1, 0x5410);
+              v[3] = __byte_perm(e1, o1, 0x7632);
+            } else {
+              constexpr uint32_t M = 0x01c001c0u, S = 0x80008000u;
+              const uint32_t w0 = h ? words[i][1] : words[i][0];
+              const uint32_t r0 = ((w0 << 6) & M) | ((w0 << 12) & S), r1 = ((w0 << 2) & M) | ((w0 << 8) & S);
+              const uint32_t r2 = ((w0 >> 2) & M) | ((w0 << 4) & S), r3 = ((w0 >> 6) & M) | (w0 & S);
+              v[0] = __byte_perm(r0, r1, 0x5410);
+              v[1] = __byte_perm(r2, r3, 0x5410);
+              v[2] = __byte_perm(r0, r1, 0x7632);
+              v[3] = __byte_perm(r2, r3, 0x7632);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[x] = mul2(mul2(v[x], f), 0x71807180u);  // 2^100
+            store16((h ? to1 : to0) + off + i * C::kRowStep * 128, v[0], v[1], v[2], v[3]);
+          }
         }
       }
     }
@@ -231,29 +389,8 @@ struct Fill {
   }
 };
 
-// Query elements 8 at a time (16 bytes, memory order) in the order of the tiles' elements.
-template <int FMT>
-__device__ __forceinline__ void order8(uint4 v, uint32_t (&x)[4]) {
-  if (FMT == RING_ATTN_CACHE_BF16) {
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-  } else if (FMT == RING_ATTN_CACHE_MXFP8) {
-    x[0] = __byte_perm(v.x, v.y, 0x5410); x[1] = __byte_perm(v.x, v.y, 0x7632);
-    x[2] = __byte_perm(v.z, v.w, 0x5410); x[3] = __byte_perm(v.z, v.w, 0x7632);
-  } else {
-    x[0] = __byte_perm(v.x, v.z, 0x5410); x[1] = __byte_perm(v.x, v.z, 0x7632);
-    x[2] = __byte_perm(v.y, v.w, 0x5410); x[3] = __byte_perm(v.y, v.w, 0x7632);
-  }
-}
-// Place of head dimension e (of 8) among the tiles' elements.
-template <int FMT>
-__host__ __device__ constexpr int place8(int e) {
-  return FMT == RING_ATTN_CACHE_BF16 ? e
-         : FMT == RING_ATTN_CACHE_MXFP8 ? (e & 4) + (e % 4 == 1 ? 2 : (e % 4 == 2 ? 1 : e % 4))
-                                        : (e < 4 ? 2 * e : 2 * (e - 4) + 1);
-}
-
 template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_constant__ Params p) {
   using C = Cfg<FMT, D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Walk s_walk;
@@ -261,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const Params p)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + kNumBars * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + kNumBars * 8 + 8);
+  volatile uint8_t* s_wide = reinterpret_cast<volatile uint8_t*>(smem + C::kOffBar + kNumBars * 8 + 16);  // [2][kFlags]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
@@ -271,13 +409,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const Params p)
       mbar_init(&bars[kKFree + b], 1);
       mbar_init(&bars[kVFree + b], 1);
       mbar_init(&bars[kSFull + b], 1);
-      mbar_init(&bars[kPReady + b], kSoftmaxWarps);
+      mbar_init(&bars[kPReady + b], kSoftmaxWarps / 2);
     }
     mbar_init(&bars[kPvDone], 1);
     mbar_init(&bars[kQReady], kSoftmaxWarps);
     mbar_init(&bars[kODone], 1);
     mbar_init(&bars[kDrain], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[kPair + i], 2);
+    for (int i = 0; i < 8; ++i) mbar_init(&bars[kMax + i], 1);
+    for (int i = 0; i < kMaxRaw; ++i) {
+      mbar_init(&bars[kRawFull + i], 1);
+      mbar_init(&bars[kRawFree + i], 2 * kFillWarps);
+      mbar_init(&bars[kRawSeen + i], 1);
+      mbar_init(&bars[kRawSeen + kMaxRaw + i], 1);
+    }
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -293,146 +438,162 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const Params p)
   const Watchdog wd{abort_flag, p.status, p.watchdog_ns};
   const uint32_t sbase = smem_u32(smem);
 
-  if (warp >= kFillWarp) {
+  auto all = [&](bool r) { return __all_sync(0xffffffffu, r) != 0; };
+  // every warp of a warpgroup takes the same branch up to its setmaxnreg
+  if (warp >= kMmaWarp) {
+    regs_decrease<kRegsOther>();
+    if (warp == kMmaWarp) {
+      // ------------------------------------------------------------------ products
+      const bool issuer = elect_one_sync();
+      Walk walk = s_walk;
+      Part part;
+      int t0 = 0, parts = 0;
+      bool ok = true;
+      while (ok && next_part(p, walk, part)) {
+        const int n_tiles = part.q1 - part.q0;
+        auto issue_s = [&](int t) -> bool {
+          if (!(wait_bar(&bars[kKFull + (t & 1)], (uint32_t)(t >> 1 & 1), wd))) return false;
+          tc_fence_after();
+          const uint64_t dk = smem_desc_sw128(sbase + (t & 1) * C::kTileBytes, 0, 1024);
+          const bool half = C::kMx && !s_wide[t % kFlags];
+          const uint32_t qa = tmem + (half || !C::kMx ? kColQ : kColQb);
+          const uint32_t desc = half ? C::kIdescS & ~C::kBf16Types : C::kIdescS;
+  #pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            if (issuer)
+              mma_ts(tmem + 128 * (t & 1), qa + 8 * k, dk + (uint64_t)(((k / 4) * kBoxBytes + (k % 4) * 32) >> 4), desc, k > 0);
+          if (issuer) {
+            mma_commit(&bars[kSFull + (t & 1)]);
+            mma_commit(&bars[kKFree + (t & 1)]);
+          }
+          return true;
+        };
+        if (!(ok = (wait_bar(&bars[kQReady], (uint32_t)(parts & 1), wd)))) break;
+        tc_fence_after();
+        ok = issue_s(t0);
+        if (ok && n_tiles > 1) ok = issue_s(t0 + 1);
+        for (int n = 0; ok && n < n_tiles; ++n) {
+          const int t = t0 + n;
+          if (!(ok = (wait_bar(&bars[kVFull + (t & 1)], (uint32_t)(t >> 1 & 1), wd)))) break;
+          if (!(ok = (wait_bar(&bars[kPReady + (t & 1)], (uint32_t)(t >> 1 & 1), wd)))) break;
+          tc_fence_after();
+          const uint64_t dv = smem_desc_sw128(sbase + C::kOffV + (t & 1) * C::kTileBytes, kBoxBytes, 1024);
+          const uint32_t desc = C::kMx && !s_wide[kFlags + t % kFlags] ? C::kIdescO & ~C::kBf16Types : C::kIdescO;
+  #pragma unroll
+          for (int k = 0; k < TK / 16; ++k)
+            if (issuer)
+              mma_ts(tmem + kColO, tmem + 128 * (t & 1) + 64 * (k / 4) + 8 * (k % 4), dv + (uint64_t)((k * 16 * 128) >> 4),
+                     desc, !(n == 0 && k == 0));
+          if (issuer) {
+            mma_commit(&bars[kPvDone]);
+            mma_commit(&bars[kVFree + (t & 1)]);
+            if (n + 1 == n_tiles) mma_commit(&bars[kODone]);
+          }
+          if (n + 2 < n_tiles && !(ok = issue_s(t + 2))) break;
+        }
+        t0 += n_tiles;
+        ++parts;
+      }
+      // every product this thread issued must finish before tensor memory is released
+      if (issuer) mma_commit(&bars[kDrain]);
+      const uint64_t since = global_timer_ns();
+      while (!mbar_try_wait(&bars[kDrain], 0)) {
+        if (global_timer_ns() - since > p.watchdog_ns) break;
+      }
+    } else if (warp == kFetchWarp) {
+      // ------------------------------------------------------------------ fetch raw tiles
+      if constexpr (C::kMx) {
+        TileIter it;
+        it.start(s_walk);
+        int t = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (; it.next(p); ++t) {
+          const int slot = t % C::kRaw;
+          if (!(ok = wait_bar(&bars[kRawFree + slot], (uint32_t)(t / C::kRaw & 1) ^ 1, wd))) break;
+          if (lane == 0) Fill<FMT, D>::fetch(p, it, smem + C::kOffRaw + slot * C::kRawBytes, &bars[kRawFull + slot]);
+        }
+        if (!ok) {
+          // wind down: this CTA's own copies must land before its shared memory goes away
+          const uint64_t since = global_timer_ns();
+          for (int x = t > C::kRaw ? t - C::kRaw : 0; x < t; ++x)
+            while (!mbar_try_wait(&bars[kRawFull + x % C::kRaw], (uint32_t)(x / C::kRaw & 1)) &&
+                   global_timer_ns() - since <= p.watchdog_ns) {
+            }
+        }
+      }
+    } else {
+      if constexpr (C::kMx) {
+        // ------------------------------------------------------------------ their scales
+        const int kv = warp - kScaleWarp;
+        TileIter it;
+        it.start(s_walk);
+  #pragma unroll 1
+        for (int t = 0; it.next(p); ++t) {
+          const int slot = t % C::kRaw;
+          if (!wait_bar(&bars[kRawFull + slot], (uint32_t)(t / C::kRaw & 1), wd)) break;
+          const bool out = Fill<FMT, D>::wide(p, it, smem + C::kOffRaw + slot * C::kRawBytes, kv);
+          if (lane == 0) {
+            s_wide[kv * kFlags + t % kFlags] = out;
+            mbar_arrive(&bars[kRawSeen + kv * kMaxRaw + slot]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else if (warp >= kFillWarp) {
+    regs_decrease<kRegsFill>();
     // ------------------------------------------------------------------ fill the tiles
-    const int ct = threadIdx.x - 32 * kFillWarp;
     using F = Fill<FMT, D>;
+    const int kv = warp >= kFillWarp + kFillWarps ? 1 : 0;
+    const int ct = (threadIdx.x - 32 * kFillWarp) % kFill;
+    const uint32_t tile0 = sbase + kv * C::kOffV;
+    uint64_t* full = &bars[kv ? kVFull : kKFull];
+    uint64_t* free = &bars[kv ? kVFree : kKFree];
     TileIter it;
-    it.begin(p, s_walk);
-    auto all = [&](bool r) { return __all_sync(0xffffffffu, r) != 0; };
+    it.start(s_walk);
     auto ready = [&](uint64_t* bar) {  // this warp's part is written: visible to the products
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
     if constexpr (C::kMx) {
-      const uint32_t raw = sbase + C::kOffRaw;
-      int fetched = 0;
-      auto fetch = [&]() {
-        if (it.valid) {
-          F::fetch(p, it, raw + (fetched % C::kRaw) * C::kRawBytes, ct);
-          it.next(p);
-          ++fetched;
-        }
-        copy_commit();
-      };
 #pragma unroll 1
-      for (int i = 0; i < C::kRaw - 1; ++i) fetch();
-#pragma unroll 1
-      for (int t = 0;; ++t) {
-        fetch();
-        if (t >= fetched) break;
-        copy_wait<C::kRaw - 1>();
-        const uint32_t slot = raw + (t % C::kRaw) * C::kRawBytes;
-        const uint32_t par = (uint32_t)(t >> 1 & 1) ^ 1;
-        if (!all(mbar_wait(&bars[kKFree + (t & 1)], par, wd))) break;
-        F::convert(slot, 0, sbase + (t & 1) * C::kTileBytes, ct);
-        ready(&bars[kKFull + (t & 1)]);
-        if (!all(mbar_wait(&bars[kVFree + (t & 1)], par, wd))) break;
-        F::convert(slot, 1, sbase + C::kOffV + (t & 1) * C::kTileBytes, ct);
-        ready(&bars[kVFull + (t & 1)]);
+      for (int t = 0; it.next(p); ++t) {
+        const int slot = t % C::kRaw;
+        if (!(wait_bar(&bars[kRawSeen + kv * kMaxRaw + slot], (uint32_t)(t / C::kRaw & 1), wd))) break;
+        // the bulk copies' own barrier: their bytes are visible to those who wait on it
+        if (!(wait_bar(&bars[kRawFull + slot], (uint32_t)(t / C::kRaw & 1), wd))) break;
+        if (!(wait_bar(&free[t & 1], (uint32_t)(t >> 1 & 1) ^ 1, wd))) break;
+        F::convert(p, it, smem + C::kOffRaw + slot * C::kRawBytes, kv, s_wide[kv * kFlags + t % kFlags] != 0,
+                   tile0 + (t & 1) * C::kTileBytes, ct);
+        ready(&full[t & 1]);
+        if (lane == 0) mbar_arrive(&bars[kRawFree + slot]);
       }
-      copy_wait<0>();
     } else {
       int t = 0;
       bool ok = true;
-      for (; it.valid; ++t) {
-        const uint32_t par = (uint32_t)(t >> 1 & 1) ^ 1;
-        if (!(ok = all(mbar_wait(&bars[kKFree + (t & 1)], par, wd)))) break;
-        F::copy_tile(p, it, p.c.k, sbase + (t & 1) * C::kTileBytes, ct);
+#pragma unroll 1
+      for (; it.next(p); ++t) {
+        if (!(ok = (wait_bar(&free[t & 1], (uint32_t)(t >> 1 & 1) ^ 1, wd)))) break;
+        F::copy_tile(p, it, kv ? p.c.v : p.c.k, tile0 + (t & 1) * C::kTileBytes, ct);
         copy_commit();
-        if (t > 0) {  // the tile before: its K and V have landed once only this K is in flight
+        if (t > 0) {  // the tile before has landed once only this one is in flight
           copy_wait<1>();
-          ready(&bars[kKFull + (t - 1 & 1)]);
-          ready(&bars[kVFull + (t - 1 & 1)]);
+          ready(&full[(t - 1) & 1]);
         }
-        if (!(ok = all(mbar_wait(&bars[kVFree + (t & 1)], par, wd)))) break;
-        F::copy_tile(p, it, p.c.v, sbase + C::kOffV + (t & 1) * C::kTileBytes, ct);
-        copy_commit();
-        it.next(p);
       }
       copy_wait<0>();
-      if (ok && t > 0) {
-        ready(&bars[kKFull + (t - 1 & 1)]);
-        ready(&bars[kVFull + (t - 1 & 1)]);
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ products
-    const bool issuer = elect_one_sync();
-    auto all = [&](bool r) { return __all_sync(0xffffffffu, r) != 0; };
-    Walk walk = s_walk;
-    Part part;
-    int t0 = 0, parts = 0;
-    bool ok = true;
-    while (ok && next_part(p, walk, part)) {
-      const int n_tiles = part.q1 - part.q0;
-      auto issue_s = [&](int t) -> bool {
-        if (!all(mbar_wait(&bars[kKFull + (t & 1)], (uint32_t)(t >> 1 & 1), wd))) return false;
-        tc_fence_after();
-        const uint64_t dk = smem_desc_sw128(sbase + (t & 1) * C::kTileBytes, 0, 1024);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          if (issuer)
-            mma_ts(tmem + 128 * (t & 1), tmem + kColQ + 8 * k, dk + (uint64_t)(((k / 4) * kBoxBytes + (k % 4) * 32) >> 4),
-                   C::kIdescS, k > 0);
-        if (issuer) {
-          mma_commit(&bars[kSFull + (t & 1)]);
-          mma_commit(&bars[kKFree + (t & 1)]);
-        }
-        return true;
-      };
-      if (!(ok = all(mbar_wait(&bars[kQReady], (uint32_t)(parts & 1), wd)))) break;
-      tc_fence_after();
-      ok = issue_s(t0);
-      if (ok && n_tiles > 1) ok = issue_s(t0 + 1);
-      for (int n = 0; ok && n < n_tiles; ++n) {
-        const int t = t0 + n;
-        if (!(ok = all(mbar_wait(&bars[kVFull + (t & 1)], (uint32_t)(t >> 1 & 1), wd)))) break;
-        if (!(ok = all(mbar_wait(&bars[kPReady + (t & 1)], (uint32_t)(t >> 1 & 1), wd)))) break;
-        tc_fence_after();
-        const uint64_t dv = smem_desc_sw128(sbase + C::kOffV + (t & 1) * C::kTileBytes, kBoxBytes, 1024);
-#pragma unroll
-        for (int k = 0; k < TK / 16; ++k)
-          if (issuer)
-            mma_ts(tmem + kColO, tmem + 128 * (t & 1) + 8 * k, dv + (uint64_t)((k * 16 * 128) >> 4), C::kIdescO,
-                   !(n == 0 && k == 0));
-        if (issuer) {
-          mma_commit(&bars[kPvDone]);
-          mma_commit(&bars[kVFree + (t & 1)]);
-          if (n + 1 == n_tiles) mma_commit(&bars[kODone]);
-        }
-        if (n + 2 < n_tiles && !(ok = issue_s(t + 2))) break;
-      }
-      t0 += n_tiles;
-      ++parts;
-    }
-    // every product this thread issued must finish before tensor memory is released
-    if (issuer) mma_commit(&bars[kDrain]);
-    const uint64_t since = global_timer_ns();
-    while (!mbar_try_wait(&bars[kDrain], 0)) {
-      if (global_timer_ns() - since > p.watchdog_ns) break;
+      if (ok && t > 0) ready(&full[(t - 1) & 1]);
     }
   } else {
+    regs_increase<kRegsSoftmax>();
     // ------------------------------------------------------------------ softmax and epilogue
-    const int wq = warp % 4, hh = warp / 4;
-    const int r = 32 * wq + lane;  // row of the group
+    const int wq = warp % 4, hh = warp / 4;  // hh: this warp's tiles are those with t % 2 == hh
+    const int r = 32 * wq + lane;            // row of the group
     const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
-    float* s_x = reinterpret_cast<float*>(smem + C::kOffMax);  // [use & 1][half][row]
-    int uses = 0;                                              // of the pair's exchange
-    // hands this row's value to the warp with the other half of its keys and takes that one's
-    auto exchange = [&](float mine, float& other) -> bool {
-      float* at = s_x + (uses & 1) * 256;
-      at[hh * 128 + r] = mine;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kPair + wq]);
-      if (!mbar_wait(&bars[kPair + wq], (uint32_t)(uses & 1), wd)) return false;
-      tc_fence_after();
-      other = at[(hh ^ 1) * 128 + r];
-      ++uses;
-      return true;
-    };
+    float* s_m = reinterpret_cast<float*>(smem + C::kOffMax);  // [t % 2][row]: the row's reference after tile t
+    float* s_x = s_m + 256;                                    // [half][row]
     Walk walk = s_walk;
     Part part;
     int t0 = 0, parts = 0;
@@ -443,23 +604,55 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const Params p)
       const int row = part.grp * TM + r;
       const bool live = row < ks.cnt * p.rep;
       const int node = live ? row / p.rep : 0;
+      float score_scale = p.scale_log2;
       {
-        // half a query row into tensor memory
+        // half a query row into tensor memory (with codes: in fp16, times 2^(14 - exponent of
+        // the row's largest element), and the same in bf16)
         const uint16_t* src = p.q + part.b * p.qs_b + (int64_t)(part.kvh * p.rep + (live ? row % p.rep : 0)) * p.qs_h +
-                              node * p.qs_t + hh * (D / 2);
+                              node * p.qs_t;
         uint32_t x[D / 4];
+        float up = 1.f;
+        if (C::kMx) {
+          uint32_t top = 0;
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+          }
+          const int e = max((int)(top >> 7), 15) - 127;  // not below 2^-112
+          up = pow2i(14 - e);
+          score_scale = p.scale_log2 * exp2f((float)(e - 14 - C::kBias));
+        }
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-          const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-          uint32_t y[4];
-          order8<FMT>(v, y);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[4 * c + e] = C::kMx ? mul2(y[e], 0x53805380u) : y[e];  // 2^40
+          const uint4 v = live ? *reinterpret_cast<const uint4*>(src + hh * (D / 2) + 8 * c) : make_uint4(0, 0, 0, 0);
+          x[4 * c] = v.x;
+          x[4 * c + 1] = v.y;
+          x[4 * c + 2] = v.z;
+          x[4 * c + 3] = v.w;
         }
-        if constexpr (D == 128)
-          tmem_st32(tmem + lane_off + kColQ + 32 * hh, x);
-        else
-          tmem_st16(tmem + lane_off + kColQ + 16 * hh, x);
+        auto put = [&](uint32_t col) {
+          if constexpr (D == 128)
+            tmem_st32(tmem + lane_off + col + 32 * hh, x);
+          else
+            tmem_st16(tmem + lane_off + col + 16 * hh, x);
+        };
+        if (C::kMx) {
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e)
+            x[e] = pack_f16x2(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xffff0000u) * up);
+          put(kColQ);
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e) {  // (exact: 8 significant bits)
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
+            x[e] = pack_bf16x2(f.x, f.y);
+          }
+          put(kColQb);
+        } else {
+          put(kColQ);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -470,71 +663,100 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const Params p)
       int depth;
       node_of(nodes, node, seen, depth);
       const int lo_key = p.window > 0 ? ks.n + depth - p.window + 1 : 0;
-      float m = -INFINITY, l = 0.f;  // reference (a whole number), sum of this half
+      // this warp's part of the row's sum, relative to the reference m (a whole number) of its
+      // last tile
+      float m = -INFINITY, l = 0.f;
       for (int n = 0; n < n_tiles; ++n) {
         const int t = t0 + n;
+        if ((t & 1) != hh) continue;
         const int kb = step_key(p, ks, part.q0 + n);
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[kSFull + (t & 1)], (uint32_t)(t >> 1 & 1), wd)) != 0)) break;
+        if (!(ok = (wait_bar(&bars[kSFull + hh], (uint32_t)(t >> 1 & 1), wd)))) break;
         tc_fence_after();
-        const uint32_t tS = tmem + lane_off + 128 * (t & 1);
-        uint32_t sr[64];
-        tmem_ld32(tS + 64 * hh, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-        tmem_ld32(tS + 64 * hh + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-        tmem_wait_ld();
+        const uint32_t tS = tmem + lane_off + 128 * hh;
         // every row sees the whole tile
         const bool whole = kb + TK <= ks.n &&
-                           (p.window <= 0 || kb + TK <= p.sinks || (int64_t)kb >= (int64_t)ks.n + p.T - p.window);
-        if (!whole) {
-          const int hi = clip((int64_t)ks.n - kb), lo = clip((int64_t)lo_key - kb), sk = min(clip((int64_t)p.sinks - kb), hi);
+                           (p.window <= 0 || kb + TK <= p.sinks || kb >= ks.n + p.T - p.window);
+        uint32_t sr[64];
+        const int hi = clip(ks.n - kb), lo = clip(lo_key - kb), sk = min(clip(p.sinks - kb), hi);
+        auto load = [&](int c0) {  // columns c0 .. c0 + 63
+          tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+          tmem_ld32(tS + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+          tmem_wait_ld();
+          if (__builtin_expect(!whole, 0)) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int c0 = 64 * hh + 32 * c;
-            const int64_t j0 = (int64_t)kb + c0 - ks.n;  // drafted node of the chunk's first column
-            const uint32_t drafts = j0 >= 64 || j0 <= -32 ? 0u : (uint32_t)(j0 >= 0 ? seen >> j0 : seen << -j0);
-            const uint32_t see = span_bits(lo, hi, c0) | span_bits(0, sk, c0) | drafts;
+            for (int c = 0; c < 2; ++c) {
+              const int c1 = c0 + 32 * c;
+              const int j0 = kb + c1 - ks.n;  // drafted node of the chunk's first column
+              const uint32_t drafts = j0 >= 64 || j0 <= -32 ? 0u : (uint32_t)(j0 >= 0 ? seen >> j0 : seen << -j0);
+              const uint32_t see = span_bits(lo, hi, c1) | span_bits(0, sk, c1) | drafts;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(see >> e & 1)) sr[32 * c + e] = 0xff800000u;  // -inf
+              for (int e = 0; e < 32; ++e)
+                if (!(see >> e & 1)) sr[32 * c + e] = 0xff800000u;  // -inf
+            }
           }
+        };
+        float top = -INFINITY;
+#pragma unroll 1  // (one copy of the code each: the roles share the instruction caches)
+        for (int c0 = 0; c0 < TK; c0 += 64) {
+          load(c0);
+          top = fmaxf(top, raw_rowmax<64>(sr));
         }
-        const float mine = raw_rowmax<64>(sr) * p.scale_log2;
-        float other;
-        if (!(ok = __all_sync(0xffffffffu, exchange(mine, other)) != 0)) break;
-        const float top = fmaxf(mine, other);
-        bool moved = false;
-        float alpha = 1.f;
-        if (top > m + kRescale || (m == -INFINITY && top != -INFINITY)) {
-          const float to = ceilf(top);
-          alpha = m == -INFINITY ? 0.f : ex2_approx(m - to);
-          l *= alpha;
-          m = to;
-          moved = true;
+        top *= score_scale;
+        // the reference after the tile before, from the other warp of these rows
+        float before = -INFINITY;
+        if (n > 0) {
+          if (!(ok = (wait_bar(&bars[kMax + 2 * wq + (hh ^ 1)], (uint32_t)((t - 1) >> 1 & 1), wd)))) break;
+          before = s_m[(hh ^ 1) * 128 + r];
+        }
+        const bool moved = top > before + C::kRescale || (before == -INFINITY && top != -INFINITY);
+        const float now = moved ? ceilf(top) : before;
+        s_m[hh * 128 + r] = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kMax + 2 * wq + hh]);
+        if (m != now) {
+          l = m == -INFINITY ? 0.f : l * ex2_approx(m - now);
+          m = now;
         }
         if (n > 0 && __any_sync(0xffffffffu, moved)) {
           // S of this tile was issued before the last P V: O must hold every product so far
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[kPvDone], (uint32_t)((t - 1) & 1), wd)) != 0)) break;
+          if (!(ok = (wait_bar(&bars[kPvDone], (uint32_t)((t - 1) & 1), wd)))) break;
           tc_fence_after();
-          rescale_o<D / 2>(tmem + lane_off + kColO + hh * (D / 2), alpha);
+          rescale_o<D>(tmem + lane_off + kColO, !moved ? 1.f : (before == -INFINITY ? 0.f : ex2_approx(before - now)));
         }
-        uint32_t pk[32];
-        l += exp_pack<64, 0>(sr, p.scale_log2, m == -INFINITY ? 0.f : m - C::kLift, pk);
-        // packed P takes the columns of keys that both halves have loaded (see exchange)
-        tmem_st32(tS + 32 * hh, pk);
+        const float sub = m == -INFINITY ? 0.f : m - C::kLift;
+        // (the last columns are still in registers: they go first)
+        const bool half = C::kMx && !s_wide[kFlags + t % kFlags];
+#pragma unroll 1
+        for (int c0 = 64; c0 >= 0; c0 -= 64) {
+          if (c0 == 0) load(0);
+          uint32_t pk[32];
+          l += exp_pack_as(sr, score_scale, sub, half, pk);
+          tmem_st32(tS + c0, pk);  // P of columns c0 .. takes the first half of their place
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kPReady + (t & 1)]);
+        if (lane == 0) mbar_arrive(&bars[kPReady + hh]);
       }
       if (!ok) break;
-      float l_other;
-      if (!(ok = __all_sync(0xffffffffu, exchange(l, l_other)) != 0)) break;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars[kODone], (uint32_t)(parts & 1), wd)) != 0)) break;
+      // the two warps of the rows join their sums (m never falls: the larger one is the row's)
+      s_x[hh * 128 + r] = l;
+      s_m[hh * 128 + r] = m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kPair + wq]);
+      if (!(ok = (wait_bar(&bars[kPair + wq], (uint32_t)(parts & 1), wd)))) break;
+      const float m_other = s_m[(hh ^ 1) * 128 + r], l_other = s_x[(hh ^ 1) * 128 + r];
+      const float m_row = fmaxf(m, m_other);
+      l = m == -INFINITY ? 0.f : l * ex2_approx(m - m_row);
+      const float lo2 = m_other == -INFINITY ? 0.f : l_other * ex2_approx(m_other - m_row);
+      m = m_row;
+      if (!(ok = (wait_bar(&bars[kODone], (uint32_t)(parts & 1), wd)))) break;
       tc_fence_after();
-      const float down = C::kMx ? 0x1p-40f : 1.f;  // l carries 2^40
-      const float L = (hh == 0 ? l + l_other : l_other + l) * down;
+      // l carries the same 2^kLift as O
+      const float L = hh == 0 ? l + lo2 : lo2 + l;  // the same sum in both
       const bool none = m == -INFINITY;
-      const float inv = none ? 0.f : 1.f / L;
-      const float lse2 = none ? -INFINITY : m + log2f(L);
+      const float inv = none ? 0.f : pow2i(-C::kBias) / L;  // O carries V's factor as well
+      const float lse2 = none ? -INFINITY : m + log2f(L * (C::kMx ? 0x1p-9f : 1.f));
       const int64_t slot = (int64_t)blockIdx.x + part.unit;
       const int64_t orow = live ? out_row(p, part.b, part.kvh, row) : 0;
 #pragma unroll 1
@@ -545,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const Params p)
         if (live) {
           float v[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[(e & ~7) + place8<FMT>(e & 7)]) * inv;
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * inv;
           const int d0 = hh * (D / 2) + 32 * c;
           if (part.alone) {
             uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + d0);
@@ -587,6 +809,9 @@ int launch(const Params& p, cudaStream_t stream) {
   auto kern = tree_tiles_kernel<FMT, D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return RING_ATTN_ECUDA;
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return RING_ATTN_ECUDA;
+  if (fa.numRegs * kThreads < 128 * (2 * kRegsSoftmax + 2 * kRegsFill + kRegsOther)) return RING_ATTN_EUNSUPPORTED;
   kern<<<p.ctas, kThreads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
 }

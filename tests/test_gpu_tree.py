@@ -6,8 +6,8 @@ once more (2^-8 |O| <= 2^-8 A); a score is a sum of D products accumulated in fp
 most D 2^-23 E (twice the half-step bound, for a truncating adder), and enters a weight and
 the weights' sum (2 D 2^-23 E A); 2^x is good to 2^-22, sums and rescales to a few 2^-23 (the
 2^-16 covers them at these lengths). A microscaled cache may be read with the weights in fp16
-(11 bits, better than bf16's 8) scaled so that its smallest step is 2^-34: a weight below 2^-24 is
-off by at most 2^-35 of the row's largest, which adds 2^-35 |v| per key, whatever A is.
+(11 bits, better than bf16's 8) scaled so that its smallest step is 2^-33: a weight below 2^-23 is
+off by at most 2^-34 of the row's largest, which adds 2^-34 |v| per key, whatever A is.
 """
 import numpy as np
 import pytest
@@ -66,12 +66,12 @@ def random_tree(B, T, seed):
 
 
 def weight_floor(cache, vals, lengths, T):
-    """2^-35 sum |v| over a sequence's keys, at most (0 for bf16 rows)."""
+    """2^-34 sum |v| over a sequence's keys, at most (0 for bf16 rows)."""
     if cache.format == "bf16":
         return 0.0
     top = max(np.abs(vals[1][b, :, :n + T]).max(initial=0, where=np.isfinite(vals[1][b, :, :n + T])) * (n + T)
               for b, n in enumerate(lengths))
-    return 2.0 ** -35 * top
+    return 2.0 ** -34 * top
 
 
 def run(q, cache, vals, lengths, parents=None, counts=None, window=0, sinks=0, scale=None, what="", floor=None):
