@@ -22,6 +22,26 @@ def _stream_ptr(stream) -> int:
     return int(s.cuda_stream)
 
 
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, device) -> int:
+    """Handle of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return int(stream.cuda_stream)
+    if _current_raw_stream is not None:
+        return _current_raw_stream(device.index)
+    return int(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _call_on(device, fn, *args) -> int:
+    """fn(*args) with `device` current (a kernel launches on the current device)."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
 def _layout(layout) -> int:
     return _LAYOUTS[layout] if isinstance(layout, str) else int(layout)
 
@@ -256,19 +276,19 @@ def _check_window(q, k, v, window, sinks):
         raise ValueError("window must be >= 1 and sinks >= 0")
 
 
-def _like(t, ref, name, shape, dtype):
+def _like(t, device, name, shape, dtype):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=ref.device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != ref.device or not t.is_contiguous():
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the inputs' device")
     return t
 
 
-def _window_scratch(workspace, need, device):
+def _scratch(workspace, need, device):
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace.device != device:
-        raise ValueError("workspace must be on the inputs' device")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     return workspace
 
 
@@ -282,13 +302,13 @@ def window_attention(q, k, v, window: int, sinks: int = 0, scale: float | None =
     _check_window(q, k, v, window, sinks)
     B, Hq, S, D = q.shape
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    out = _like(out, q, "out", (B, Hq, S, D), torch.bfloat16)
-    lse = _like(lse, q, "lse", (B, Hq, S), torch.float32)
-    workspace = _window_scratch(workspace, 256, q.device)
-    with torch.cuda.device(q.device):
-        rc = _b.ring_attn_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq,
-                                     k.shape[1], S, D, int(window), int(sinks), scale, workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    dev = q.device
+    out = _like(out, dev, "out", (B, Hq, S, D), torch.bfloat16)
+    lse = _like(lse, dev, "lse", (B, Hq, S), torch.float32)
+    workspace = _scratch(workspace, 256, dev)
+    rc = _call_on(dev, _b.ring_attn_window_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                  lse.data_ptr(), B, Hq, k.shape[1], S, D, int(window), int(sinks), scale, workspace.data_ptr(),
+                  workspace.nbytes, _stream_on(stream, dev))
     _b.check(rc, "ring_attn_window_fwd")
     return out, lse
 
@@ -307,18 +327,18 @@ def window_attention_backward(q, k, v, out, lse, dout, window: int, sinks: int =
     if lse.shape != (B, Hq, S) or lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [B, Hq, S] tensor")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    dev = q.device
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if workspace is None:
         need = _b.ring_attn_window_bwd_workspace_bytes(B, Hq, k.shape[1], S, D, int(window), int(sinks))
         if need == 0:
             raise _b.RingAttnError(_b.EINVAL, "ring_attn_window_bwd_workspace_bytes")
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    workspace = _window_scratch(workspace, 0, q.device)
-    with torch.cuda.device(q.device):
-        rc = _b.ring_attn_window_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                     dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, k.shape[1], S,
-                                     D, int(window), int(sinks), scale, workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        workspace = _scratch(workspace, 0, dev)
+    rc = _call_on(dev, _b.ring_attn_window_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                  lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, k.shape[1], S, D,
+                  int(window), int(sinks), scale, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
     _b.check(rc, "ring_attn_window_bwd")
     return dq, dk, dv
 

@@ -216,14 +216,13 @@ def ring_attn_decode(q, k, v, out, lse, B, Hq, Hkv, S, D, P, layout, scale, dtyp
                                    workspace_bytes, stream)
 
 
-def _strides(values):
-    return (_c_i64 * len(values))(*values)
+_Strides3, _Strides6 = _c_i64 * 3, _c_i64 * 6
 
 
 def ring_attn_cache_write(k_new, v_new, strides, dtype, k_cache, v_cache, k_scale, v_scale, format_, B, Hkv, capacity,
                           D, T, T_src, start, count, index, workspace, workspace_bytes, stream) -> int:
     """strides: six element strides, (b, h, t) of k_new and of v_new."""
-    return load().ring_attn_cache_write(k_new, v_new, _strides(strides), dtype, k_cache, v_cache, k_scale, v_scale,
+    return load().ring_attn_cache_write(k_new, v_new, _Strides6(*strides), dtype, k_cache, v_cache, k_scale, v_scale,
                                         format_, B, Hkv, capacity, D, T, T_src, start, count, index, workspace,
                                         workspace_bytes, stream)
 
@@ -241,7 +240,7 @@ def ring_attn_tree_workspace_bytes(format_, B, Hq, Hkv, capacity, D, T) -> int:
 def ring_attn_tree(q, q_strides, k_cache, v_cache, k_scale, v_scale, format_, out, lse, B, Hq, Hkv, capacity, D, T,
                    lengths, parents, counts, window, sinks, scale, workspace, workspace_bytes, stream) -> int:
     """q_strides: three element strides, (b, h, t)."""
-    return load().ring_attn_tree(q, _strides(q_strides), k_cache, v_cache, k_scale, v_scale, format_, out, lse, B, Hq,
+    return load().ring_attn_tree(q, _Strides3(*q_strides), k_cache, v_cache, k_scale, v_scale, format_, out, lse, B, Hq,
                                  Hkv, capacity, D, T, lengths, parents, counts, window, sinks, scale, workspace,
                                  workspace_bytes, stream)
 

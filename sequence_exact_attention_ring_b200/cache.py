@@ -10,7 +10,7 @@ import math
 import torch
 
 from . import binding as _b
-from .api import _DTYPES, _stream_ptr
+from .api import _DTYPES, _call_on, _like, _scratch, _stream_on
 
 _FORMATS = {"bf16": _b.CACHE_BF16, "mxfp8": _b.CACHE_MXFP8, "mxfp4": _b.CACHE_MXFP4}
 _BLOCK = 32
@@ -71,34 +71,37 @@ class KVCache:
         return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scale, self.v_scale) if t is not None)
 
     def _pointers(self):
-        return tuple(0 if t is None else t.data_ptr() for t in (self.k, self.v, self.k_scale, self.v_scale))
+        if self.k_scale is None:
+            return self.k.data_ptr(), self.v.data_ptr(), 0, 0
+        return self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr()
 
 
-def _int_rows(t, shape, name, device, optional=True) -> int:
+def _int_rows(t, shape, name, device) -> int:
+    """Address of an int32 tensor of this shape (0 for None)."""
     if t is None:
-        if optional:
-            return 0
-        raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape) or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        return 0
+    if t.shape != shape or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on the cache's device")
     return t.data_ptr()
 
 
+def _required(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t
+
+
 def _strides(t):
     """Element strides of the first three dimensions (those of size 1 do not matter)."""
-    return tuple(s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape[:3]))
+    (n0, n1, n2, _), (s0, s1, s2, _) = t.shape, t.stride()
+    return s0 if n0 > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0
 
 
 def _on_device(cache: KVCache):
-    if cache.k.device.type != "cuda":
+    dev = cache.k.device
+    if dev.type != "cuda":
         raise ValueError("the cache must be on a CUDA device")
-    return cache.k.device
-
-
-def _stream_of(stream, device) -> int:
-    if stream is None:
-        return int(torch.cuda.current_stream(device).cuda_stream)
-    return _stream_ptr(stream)
+    return dev
 
 
 def cache_write(cache: KVCache, k_new, v_new, start, count=None, index=None, workspace=None, stream=None) -> None:
@@ -113,7 +116,7 @@ def cache_write(cache: KVCache, k_new, v_new, start, count=None, index=None, wor
     """
     dev = _on_device(cache)
     for t in (k_new, v_new):
-        if t.dim() != 4 or tuple(t.shape[:2]) != (cache.B, cache.Hkv) or t.shape[3] != cache.D:
+        if t.dim() != 4 or t.shape[0] != cache.B or t.shape[1] != cache.Hkv or t.shape[3] != cache.D:
             raise ValueError("k_new and v_new must be [B, Hkv, T, D] like the cache")
         if t.dtype not in _DTYPES or t.dtype != k_new.dtype or t.device != dev:
             raise ValueError("k_new and v_new must share dtype float32 or bfloat16 and the cache's device")
@@ -125,16 +128,14 @@ def cache_write(cache: KVCache, k_new, v_new, start, count=None, index=None, wor
     T = T_src if index is None else index.shape[-1]
     if T == 0 or T_src == 0:
         return
-    p_start = _int_rows(start, (cache.B,), "start", dev, optional=False)
+    p_start = _int_rows(_required(start, "start"), (cache.B,), "start", dev)
     p_count = _int_rows(count, (cache.B,), "count", dev)
     p_index = _int_rows(index, (cache.B, T), "index", dev)
-    with torch.cuda.device(dev):
-        rc = _b.ring_attn_cache_write(k_new.data_ptr(), v_new.data_ptr(), (*_strides(k_new), *_strides(v_new)),
-                                      _DTYPES[k_new.dtype], *cache._pointers(), _FORMATS[cache.format], cache.B,
-                                      cache.Hkv, cache.capacity, cache.D, T, T_src, p_start, p_count, p_index,
-                                      0 if workspace is None else workspace.data_ptr(),
-                                      0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                      _stream_of(stream, dev))
+    ws, ws_bytes = (0, 0) if workspace is None else (_scratch(workspace, 0, dev).data_ptr(), workspace.nbytes)
+    rc = _call_on(dev, _b.ring_attn_cache_write, k_new.data_ptr(), v_new.data_ptr(),
+                  (*_strides(k_new), *_strides(v_new)), _DTYPES[k_new.dtype], *cache._pointers(),
+                  _FORMATS[cache.format], cache.B, cache.Hkv, cache.capacity, cache.D, T, T_src, p_start, p_count,
+                  p_index, ws, ws_bytes, _stream_on(stream, dev))
     _b.check(rc, "ring_attn_cache_write")
 
 
@@ -148,23 +149,17 @@ def cache_read(cache: KVCache, start, T: int, count=None, dtype=torch.bfloat16, 
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float32 or bfloat16")
     shape = (cache.B, cache.Hkv, T, cache.D)
-    outs = []
-    for t in (k_out, v_out):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-        elif tuple(t.shape) != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-            raise ValueError("k_out and v_out must be contiguous [B, Hkv, T, D] tensors of dtype")
-        outs.append(t)
+    k_out = _like(k_out, dev, "k_out", shape, dtype)
+    v_out = _like(v_out, dev, "v_out", shape, dtype)
     if T == 0:
-        return tuple(outs)
-    p_start = _int_rows(start, (cache.B,), "start", dev, optional=False)
+        return k_out, v_out
+    p_start = _int_rows(_required(start, "start"), (cache.B,), "start", dev)
     p_count = _int_rows(count, (cache.B,), "count", dev)
-    with torch.cuda.device(dev):
-        rc = _b.ring_attn_cache_read(*cache._pointers(), _FORMATS[cache.format], cache.B, cache.Hkv, cache.capacity,
-                                     cache.D, T, p_start, p_count, outs[0].data_ptr(), outs[1].data_ptr(),
-                                     _DTYPES[dtype], _stream_of(stream, dev))
+    rc = _call_on(dev, _b.ring_attn_cache_read, *cache._pointers(), _FORMATS[cache.format], cache.B, cache.Hkv,
+                  cache.capacity, cache.D, T, p_start, p_count, k_out.data_ptr(), v_out.data_ptr(), _DTYPES[dtype],
+                  _stream_on(stream, dev))
     _b.check(rc, "ring_attn_cache_read")
-    return tuple(outs)
+    return k_out, v_out
 
 
 def tree_workspace(q, cache: KVCache) -> torch.Tensor:
@@ -196,25 +191,14 @@ def tree_attention(q, cache: KVCache, lengths, parents=None, counts=None, window
         raise ValueError("q must be a bf16 tensor on the cache's device with a contiguous head dimension")
     B, Hq, T, D = q.shape
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    if out is None:
-        out = torch.empty((B, Hq, T, D), dtype=torch.bfloat16, device=dev)
-    elif tuple(out.shape) != (B, Hq, T, D) or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != dev:
-        raise ValueError("out must be a contiguous bf16 [B, Hq, T, D] tensor")
-    if lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-    elif tuple(lse.shape) != (B, Hq, T) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
-        raise ValueError("lse must be a contiguous float32 [B, Hq, T] tensor")
-    p_len = _int_rows(lengths, (B,), "lengths", dev, optional=False)
+    out = _like(out, dev, "out", (B, Hq, T, D), torch.bfloat16)
+    lse = _like(lse, dev, "lse", (B, Hq, T), torch.float32)
+    p_len = _int_rows(_required(lengths, "lengths"), (B,), "lengths", dev)
     p_par = _int_rows(parents, (B, T), "parents", dev)
     p_cnt = _int_rows(counts, (B,), "counts", dev)
-    if workspace is None:
-        workspace = tree_workspace(q, cache)
-    elif workspace.device != dev:
-        raise ValueError("workspace must be on the cache's device")
-    with torch.cuda.device(dev):
-        rc = _b.ring_attn_tree(q.data_ptr(), _strides(q), *cache._pointers(), _FORMATS[cache.format],
-                               out.data_ptr(), lse.data_ptr(), B, Hq, cache.Hkv, cache.capacity, D, T, p_len, p_par,
-                               p_cnt, int(window), int(sinks), scale, workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), _stream_of(stream, dev))
+    workspace = tree_workspace(q, cache) if workspace is None else _scratch(workspace, 0, dev)
+    rc = _call_on(dev, _b.ring_attn_tree, q.data_ptr(), _strides(q), *cache._pointers(), _FORMATS[cache.format],
+                  out.data_ptr(), lse.data_ptr(), B, Hq, cache.Hkv, cache.capacity, D, T, p_len, p_par, p_cnt,
+                  int(window), int(sinks), scale, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
     _b.check(rc, "ring_attn_tree")
     return out, lse

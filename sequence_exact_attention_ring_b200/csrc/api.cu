@@ -491,7 +491,6 @@ int ring_attn_window_fwd(const void* q, const void* k, const void* v, void* out,
   if (!(scale > 0.f) || !isfinite(scale)) return RING_ATTN_EINVAL;
   if (!device_is_sm100()) return RING_ATTN_EUNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((rc = reset_status(workspace, st))) return rc;
   return launch_window_fwd(q, k, v, out, lse, g, scale, static_cast<int*>(workspace), watchdog_ns(), st);
 }
 
@@ -517,7 +516,6 @@ int ring_attn_window_bwd(const void* q, const void* k, const void* v, const void
   if (!(scale > 0.f) || !isfinite(scale)) return RING_ATTN_EINVAL;
   if (!device_is_sm100()) return RING_ATTN_EUNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((rc = reset_status(workspace, st))) return rc;
   float* scratch = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeaderBytes);
   return launch_window_bwd(q, k, v, out, lse, dout, dq, dk, dv, g, scale, scratch, static_cast<int*>(workspace),
                            watchdog_ns(), st);

@@ -4,8 +4,10 @@
 // once, a read the other way round. A thread owns 8 consecutive elements of a row on the
 // write side (one 16-byte load of bf16, 8 or 4 bytes of codes out), so the 32 values of
 // a scale block sit in 4 neighbouring lanes and their maximum takes two shuffles; on the
-// read side it owns the elements of one 16-byte store. K and V rows go through one
-// launch.
+// read side it owns the elements of one 16-byte store. A block takes a run of rows of one
+// (K or V, sequence, head), so that the divisions that find it are made once per block and
+// not per row (made per row they were most of a read's instructions: 2 x 65536 tokens of 8
+// heads took 209 us). K and V rows go through one launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -28,7 +30,7 @@ struct WriteParams {
   const int32_t* index;    // [B, T] or null
   int B, Hkv, T, T_src;
   int64_t capacity;
-  uint32_t rows;           // 2 * B * Hkv * T
+  uint32_t chunks;         // blocks per (K or V, sequence, head)
   int* status;             // or null
 };
 
@@ -40,14 +42,8 @@ struct ReadParams {
   const int32_t* count;
   int B, Hkv, T;
   int64_t capacity;
-  uint32_t rows;
+  uint32_t chunks;
 };
-
-// K's or V's pointer, by a select (an index into the parameters would copy them to the stack)
-template <typename P>
-__device__ __forceinline__ P pick(P const (&a)[2], int which) {
-  return which ? a[1] : a[0];
-}
 
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
@@ -69,42 +65,56 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The run of rows that a block takes: K or V (which), head bh = b * Hkv + h, rows from `first`.
+struct Run {
+  int which;
+  uint32_t b, h, first;
+};
+__device__ __forceinline__ Run block_run(uint32_t chunks, int B, int Hkv, uint32_t rows) {
+  Run r;
+  const uint32_t x = blockIdx.x / chunks;
+  r.first = (blockIdx.x - x * chunks) * rows;
+  r.which = x >= (uint32_t)(B * Hkv);
+  const uint32_t bh = r.which ? x - (uint32_t)(B * Hkv) : x;
+  r.b = bh / (uint32_t)Hkv;
+  r.h = bh - r.b * (uint32_t)Hkv;
+  return r;
+}
+
 // kRows rows per thread, their loads issued before any of them is encoded.
 template <int FMT, int D, typename T, int kRows>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ WriteParams p) {
   constexpr int kTpr = D / 8;                   // threads per row
-  constexpr int kRpb = kThreads / kTpr;         // rows per block and step
+  const uint32_t rpb = blockDim.x / kTpr;       // rows per block and step
+  const Run run = block_run(p.chunks, p.B, p.Hkv, rpb * kRows);
   const int sub = threadIdx.x % kTpr;
+  const int32_t n = p.count ? p.count[run.b] : p.T;
+  const int64_t start = p.start[run.b];
+  const bool w = run.which != 0;
+  const T* src = static_cast<const T*>(w ? p.src[1] : p.src[0]) + run.b * (w ? p.stride[1][0] : p.stride[0][0]) +
+                 run.h * (w ? p.stride[1][1] : p.stride[0][1]) + sub * 8;
+  const int64_t stride = w ? p.stride[1][2] : p.stride[0][2];
+  const int64_t head_row = ((int64_t)run.b * p.Hkv + run.h) * p.capacity;
+  uint8_t* codes = w ? p.codes[1] : p.codes[0];
+  uint8_t* scale = w ? p.scale[1] : p.scale[0];
+  if (n > p.T && p.status && threadIdx.x == 0) atomicExch(p.status, RING_ATTN_EINVAL);
   float x[kRows][8];
   int64_t dst[kRows];
-  int which[kRows];
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    const uint32_t r = (blockIdx.x * kRows + u) * (uint32_t)kRpb + threadIdx.x / kTpr;
+    const uint32_t i = run.first + u * rpb + threadIdx.x / kTpr;
     dst[u] = -1;
-    which[u] = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
-    if (r >= p.rows) continue;
-    const uint32_t i = r % (uint32_t)p.T;
-    uint32_t y = r / (uint32_t)p.T;
-    const uint32_t h = y % (uint32_t)p.Hkv;
-    y /= (uint32_t)p.Hkv;
-    const uint32_t b = y % (uint32_t)p.B;
-    which[u] = (int)(y / (uint32_t)p.B);
-    const int32_t n = p.count ? p.count[b] : p.T;
-    if ((int32_t)i >= n) continue;
-    const int64_t pos = (int64_t)p.start[b] + i;
-    const int64_t from = p.index ? (int64_t)p.index[(int64_t)b * p.T + i] : (int64_t)i;
-    if (pos < 0 || pos >= p.capacity || from < 0 || from >= p.T_src || n > p.T) {
+    if (i >= (uint32_t)p.T || (int32_t)i >= n) continue;
+    const int64_t pos = start + i;
+    const int64_t from = p.index ? (int64_t)p.index[(int64_t)run.b * p.T + i] : (int64_t)i;
+    if (pos < 0 || pos >= p.capacity || from < 0 || from >= p.T_src) {
       if (p.status && sub == 0) atomicExch(p.status, RING_ATTN_EINVAL);
-      if (pos < 0 || pos >= p.capacity || from < 0 || from >= p.T_src) continue;
+      continue;
     }
-    const bool w = which[u] != 0;
-    const int64_t off = b * (w ? p.stride[1][0] : p.stride[0][0]) + h * (w ? p.stride[1][1] : p.stride[0][1]) +
-                        from * (w ? p.stride[1][2] : p.stride[0][2]);
-    load8(static_cast<const T*>(pick(p.src, w)) + off + sub * 8, x[u]);
-    dst[u] = ((int64_t)b * p.Hkv + h) * p.capacity + pos;
+    load8(src + from * stride, x[u]);
+    dst[u] = head_row + pos;
   }
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
@@ -115,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteParams
       o.y = bf16_pair(x[u][2], x[u][3]);
       o.z = bf16_pair(x[u][4], x[u][5]);
       o.w = bf16_pair(x[u][6], x[u][7]);
-      *reinterpret_cast<uint4*>(pick(p.codes, which[u]) + dst[u] * (2 * D) + sub * 16) = o;
+      *reinterpret_cast<uint4*>(codes + dst[u] * (2 * D) + sub * 16) = o;
       continue;
     }
     // the block's largest magnitude as fp32 bits: an unsigned maximum, so a NaN is kept
@@ -137,49 +147,42 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteParams
       uint2 o;
       o.x = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
       o.y = e4m3_pair(y[4], y[5]) | (e4m3_pair(y[6], y[7]) << 16);
-      *reinterpret_cast<uint2*>(pick(p.codes, which[u]) + dst[u] * D + sub * 8) = o;
+      *reinterpret_cast<uint2*>(codes + dst[u] * D + sub * 8) = o;
     } else {
       const uint32_t o = e2m1_pair(y[0], y[1]) | (e2m1_pair(y[2], y[3]) << 8) | (e2m1_pair(y[4], y[5]) << 16) |
                          (e2m1_pair(y[6], y[7]) << 24);
-      *reinterpret_cast<uint32_t*>(pick(p.codes, which[u]) + dst[u] * (D / 2) + sub * 4) = o;
+      *reinterpret_cast<uint32_t*>(codes + dst[u] * (D / 2) + sub * 4) = o;
     }
-    if (sub % 4 == 0) pick(p.scale, which[u])[dst[u] * (D / kMxBlock) + sub / 4] = (uint8_t)byte;
+    if (sub % 4 == 0) scale[dst[u] * (D / kMxBlock) + sub / 4] = (uint8_t)byte;
   }
 }
 
 template <int FMT, int D, typename T, int kRows>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p) {
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams p) {
   constexpr int kEl = 16 / (int)sizeof(T);      // elements per thread: one 16-byte store
   constexpr int kTpr = D / kEl;
-  constexpr int kRpb = kThreads / kTpr;
   constexpr int kBytes = FMT == RING_ATTN_CACHE_BF16 ? 2 * kEl : (FMT == RING_ATTN_CACHE_MXFP8 ? kEl : kEl / 2);
+  constexpr int kWords = (kBytes + 3) / 4;
+  const uint32_t rpb = blockDim.x / kTpr;
+  const Run run = block_run(p.chunks, p.B, p.Hkv, rpb * kRows);
   const int sub = threadIdx.x % kTpr;
-  uint32_t c[kRows][(kBytes + 3) / 4];
-  uint32_t s[kRows];
-  int64_t out_row[kRows];
-  int which[kRows];
+  const int32_t n = p.count ? p.count[run.b] : p.T;
+  const int64_t start = p.start[run.b];
+  const int64_t head = (int64_t)run.b * p.Hkv + run.h;
+  const uint8_t* codes = (run.which ? p.codes[1] : p.codes[0]) + head * p.capacity * cache_row_bytes<FMT>(D) + sub * kBytes;
+  const uint8_t* scale = (run.which ? p.scale[1] : p.scale[0]) + head * p.capacity * (D / kMxBlock) + sub * kEl / kMxBlock;
+  T* out = static_cast<T*>(run.which ? p.out[1] : p.out[0]) + head * p.T * D + sub * kEl;
+  uint32_t c[kRows][kWords], s[kRows];
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    const uint32_t r = (blockIdx.x * kRows + u) * (uint32_t)kRpb + threadIdx.x / kTpr;
-    out_row[u] = -1;
-    which[u] = 0;
-    s[u] = 0;
+    const uint32_t i = run.first + u * rpb + threadIdx.x / kTpr;
+    const int64_t pos = start + i;
+    s[u] = 127u;
 #pragma unroll
-    for (int e = 0; e < (kBytes + 3) / 4; ++e) c[u][e] = 0u;
-    if (r >= p.rows) continue;
-    const uint32_t i = r % (uint32_t)p.T;
-    uint32_t y = r / (uint32_t)p.T;
-    const uint32_t h = y % (uint32_t)p.Hkv;
-    y /= (uint32_t)p.Hkv;
-    const uint32_t b = y % (uint32_t)p.B;
-    which[u] = (int)(y / (uint32_t)p.B);
-    out_row[u] = (int64_t)(r % (p.rows / 2));
+    for (int e = 0; e < kWords; ++e) c[u][e] = 0u;
     // rows past the count, or outside the cache, read as zeros
-    if (p.count && (int32_t)i >= p.count[b]) continue;
-    const int64_t pos = (int64_t)p.start[b] + i;
-    if (pos < 0 || pos >= p.capacity) continue;
-    const int64_t row = ((int64_t)b * p.Hkv + h) * p.capacity + pos;
-    const uint8_t* q = pick(p.codes, which[u]) + row * cache_row_bytes<FMT>(D) + sub * kBytes;
+    if (i >= (uint32_t)p.T || (int32_t)i >= n || pos < 0 || pos >= p.capacity) continue;
+    const uint8_t* q = codes + pos * cache_row_bytes<FMT>(D);
     if constexpr (kBytes == 16) {
       const uint4 v = *reinterpret_cast<const uint4*>(q);
       c[u][0] = v.x; c[u][1] = v.y; c[u][2] = v.z; c[u][3] = v.w;
@@ -191,11 +194,12 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p
     } else {
       c[u][0] = *reinterpret_cast<const uint16_t*>(q);
     }
-    if (FMT != RING_ATTN_CACHE_BF16) s[u] = pick(p.scale, which[u])[row * (D / kMxBlock) + sub * kEl / kMxBlock];
+    if (FMT != RING_ATTN_CACHE_BF16) s[u] = scale[pos * (D / kMxBlock)];
   }
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    if (out_row[u] < 0) continue;
+    const uint32_t i = run.first + u * rpb + threadIdx.x / kTpr;
+    if (i >= (uint32_t)p.T) continue;
     float x[kEl];
     const float f = FMT == RING_ATTN_CACHE_BF16 ? 1.f : mx_scale(s[u]);
 #pragma unroll
@@ -211,43 +215,55 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p
       x[e] = FMT == RING_ATTN_CACHE_BF16 ? v.x : v.x * f;
       x[e + 1] = FMT == RING_ATTN_CACHE_BF16 ? v.y : v.y * f;
     }
-    T* o = static_cast<T*>(pick(p.out, which[u])) + out_row[u] * D + sub * kEl;
-    uint4 w;
+    uint4 o;
     if constexpr (sizeof(T) == 2) {
-      w = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+      o = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
     } else {
-      w = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+      o = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
-    *reinterpret_cast<uint4*>(o) = w;
+    *reinterpret_cast<uint4*>(out + (int64_t)i * D) = o;
   }
 }
 
-// Rows per thread: 4 where that still leaves every SM its 8 resident blocks, else 1
-// (a single token's append is one short wave either way).
-inline int rows_per_thread(uint32_t rows, int rpb) { return rows >= 4ull * 8 * 148 * rpb ? 4 : 1; }
-
-inline unsigned blocks_for(uint32_t rows, int rpb, int per) {
-  const uint64_t n = (uint64_t)rpb * per;
-  return (unsigned)((rows + n - 1) / n);
+// A launch: `heads` = 2 B Hkv runs of T rows, `tpr` threads per row. Four rows per thread
+// where that still leaves every SM its 8 resident blocks, else one; blocks no larger than
+// their rows need (a single token's append is one small block per head either way).
+struct Launch {
+  int rows_per_thread;
+  unsigned threads, blocks;
+  uint32_t chunks;
+};
+inline Launch plan_launch(uint32_t heads, int T, int tpr) {
+  Launch l;
+  const uint64_t rows = (uint64_t)heads * T;
+  const int64_t need = ((int64_t)T * tpr + 31) / 32 * 32;  // threads that one head's rows take
+  l.rows_per_thread = rows * tpr >= 4ull * 8 * 148 * kThreads && need >= 4 * kThreads ? 4 : 1;
+  l.threads = need < kThreads ? (unsigned)need : kThreads;
+  const uint32_t per = l.threads / tpr * l.rows_per_thread;
+  l.chunks = ((uint32_t)T + per - 1) / per;
+  l.blocks = heads * l.chunks;  // at most the number of rows, below 2^31
+  return l;
 }
 
 template <int FMT, int D, typename T>
-int write_t(const WriteParams& p, cudaStream_t stream) {
-  constexpr int rpb = kThreads / (D / 8);
-  if (rows_per_thread(p.rows, rpb) == 4)
-    cache_write_kernel<FMT, D, T, 4><<<blocks_for(p.rows, rpb, 4), kThreads, 0, stream>>>(p);
+int write_t(WriteParams p, cudaStream_t stream) {
+  const Launch l = plan_launch(2u * p.B * p.Hkv, p.T, D / 8);
+  p.chunks = l.chunks;
+  if (l.rows_per_thread == 4)
+    cache_write_kernel<FMT, D, T, 4><<<l.blocks, l.threads, 0, stream>>>(p);
   else
-    cache_write_kernel<FMT, D, T, 1><<<blocks_for(p.rows, rpb, 1), kThreads, 0, stream>>>(p);
+    cache_write_kernel<FMT, D, T, 1><<<l.blocks, l.threads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
 }
 
 template <int FMT, int D, typename T>
-int read_t(const ReadParams& p, cudaStream_t stream) {
-  constexpr int rpb = kThreads / (D * (int)sizeof(T) / 16);
-  if (rows_per_thread(p.rows, rpb) == 4)
-    cache_read_kernel<FMT, D, T, 4><<<blocks_for(p.rows, rpb, 4), kThreads, 0, stream>>>(p);
+int read_t(ReadParams p, cudaStream_t stream) {
+  const Launch l = plan_launch(2u * p.B * p.Hkv, p.T, D * (int)sizeof(T) / 16);
+  p.chunks = l.chunks;
+  if (l.rows_per_thread == 4)
+    cache_read_kernel<FMT, D, T, 4><<<l.blocks, l.threads, 0, stream>>>(p);
   else
-    cache_read_kernel<FMT, D, T, 1><<<blocks_for(p.rows, rpb, 1), kThreads, 0, stream>>>(p);
+    cache_read_kernel<FMT, D, T, 1><<<l.blocks, l.threads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
 }
 
@@ -286,7 +302,6 @@ int launch_cache_write(const CacheView& c, const void* k_new, const void* v_new,
   p.T = T;
   p.T_src = T_src;
   p.capacity = c.capacity;
-  p.rows = (uint32_t)(2ll * c.B * c.Hkv * T);
   p.status = status;
   switch (c.format) {
     case RING_ATTN_CACHE_BF16: return cache::write_f<RING_ATTN_CACHE_BF16>(p, c.D, dtype, stream);
@@ -309,7 +324,6 @@ int launch_cache_read(const CacheView& c, int T, const int32_t* start, const int
   p.Hkv = c.Hkv;
   p.T = T;
   p.capacity = c.capacity;
-  p.rows = (uint32_t)(2ll * c.B * c.Hkv * T);
   switch (c.format) {
     case RING_ATTN_CACHE_BF16: return cache::read_f<RING_ATTN_CACHE_BF16>(p, c.D, dtype, stream);
     case RING_ATTN_CACHE_MXFP8: return cache::read_f<RING_ATTN_CACHE_MXFP8>(p, c.D, dtype, stream);

@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(256) window_prep_kernel(const uint16_t* __rest
                                                           const uint16_t* __restrict__ dout,
                                                           const float* __restrict__ lse, float* __restrict__ lse2,
                                                           float* __restrict__ delta, int64_t S, int64_t s_pad,
-                                                          int64_t rows) {
+                                                          int64_t rows, int* status) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = RING_ATTN_OK;
   constexpr int kTpr = D / 8;
   const int64_t row = (int64_t)blockIdx.x * (256 / kTpr) + threadIdx.x / kTpr;
   const int sub = threadIdx.x % kTpr;
@@ -749,7 +750,7 @@ int launch(const void* q, const void* k, const void* v, const void* out, const f
     return RING_ATTN_ECUDA;
   window_prep_kernel<D><<<(unsigned)prep_blocks, 256, 0, stream>>>(
       static_cast<const uint16_t*>(out), static_cast<const uint16_t*>(dout), lse, scratch, scratch + rows, g.S, p.s_pad,
-      rows);
+      rows, status);
   if (cudaGetLastError() != cudaSuccess) return RING_ATTN_ECUDA;
   p.out0 = dk;
   p.out1 = dv;

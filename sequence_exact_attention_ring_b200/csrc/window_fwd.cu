@@ -107,6 +107,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
   const WinGeom& g = p.g;
 
   if (threadIdx.x == 0) {
+    if (blockIdx.x == 0) *p.status = RING_ATTN_OK;  // (no wait can have run out yet)
     mbar_init(&bars[kQFull], 1);
     for (int q = 0; q < NQ; ++q) {
       mbar_init(&bars[kSFull + q], 1);
