@@ -30,7 +30,6 @@ struct WriteParams {
   const int32_t* index;    // [B, T] or null
   int B, Hkv, T, T_src;
   int64_t capacity;
-  uint32_t chunks;         // blocks per (K or V, sequence, head)
   int* status;             // or null
 };
 
@@ -42,7 +41,6 @@ struct ReadParams {
   const int32_t* count;
   int B, Hkv, T;
   int64_t capacity;
-  uint32_t chunks;
 };
 
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
@@ -70,10 +68,12 @@ struct Run {
   int which;
   uint32_t b, h, first;
 };
-__device__ __forceinline__ Run block_run(uint32_t chunks, int B, int Hkv, uint32_t rows) {
+__device__ __forceinline__ Run block_run(int B, int Hkv, uint32_t rows) {
+  // heads run fastest: the rows of a token of a fused projection lie side by side
   Run r;
-  const uint32_t x = blockIdx.x / chunks;
-  r.first = (blockIdx.x - x * chunks) * rows;
+  const uint32_t heads = 2u * B * Hkv, c = blockIdx.x / heads;
+  const uint32_t x = blockIdx.x - c * heads;
+  r.first = c * rows;
   r.which = x >= (uint32_t)(B * Hkv);
   const uint32_t bh = r.which ? x - (uint32_t)(B * Hkv) : x;
   r.b = bh / (uint32_t)Hkv;
@@ -86,7 +86,7 @@ template <int FMT, int D, typename T, int kRows>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ WriteParams p) {
   constexpr int kTpr = D / 8;                   // threads per row
   const uint32_t rpb = blockDim.x / kTpr;       // rows per block and step
-  const Run run = block_run(p.chunks, p.B, p.Hkv, rpb * kRows);
+  const Run run = block_run(p.B, p.Hkv, rpb * kRows);
   const int sub = threadIdx.x % kTpr;
   const int32_t n = p.count ? p.count[run.b] : p.T;
   const int64_t start = p.start[run.b];
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   constexpr int kBytes = FMT == RING_ATTN_CACHE_BF16 ? 2 * kEl : (FMT == RING_ATTN_CACHE_MXFP8 ? kEl : kEl / 2);
   constexpr int kWords = (kBytes + 3) / 4;
   const uint32_t rpb = blockDim.x / kTpr;
-  const Run run = block_run(p.chunks, p.B, p.Hkv, rpb * kRows);
+  const Run run = block_run(p.B, p.Hkv, rpb * kRows);
   const int sub = threadIdx.x % kTpr;
   const int32_t n = p.count ? p.count[run.b] : p.T;
   const int64_t start = p.start[run.b];
@@ -231,7 +231,6 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 struct Launch {
   int rows_per_thread;
   unsigned threads, blocks;
-  uint32_t chunks;
 };
 inline Launch plan_launch(uint32_t heads, int T, int tpr) {
   Launch l;
@@ -240,15 +239,13 @@ inline Launch plan_launch(uint32_t heads, int T, int tpr) {
   l.rows_per_thread = rows * tpr >= 4ull * 8 * 148 * kThreads && need >= 4 * kThreads ? 4 : 1;
   l.threads = need < kThreads ? (unsigned)need : kThreads;
   const uint32_t per = l.threads / tpr * l.rows_per_thread;
-  l.chunks = ((uint32_t)T + per - 1) / per;
-  l.blocks = heads * l.chunks;  // at most the number of rows, below 2^31
+  l.blocks = heads * (((uint32_t)T + per - 1) / per);  // at most the number of rows, below 2^31
   return l;
 }
 
 template <int FMT, int D, typename T>
 int write_t(WriteParams p, cudaStream_t stream) {
   const Launch l = plan_launch(2u * p.B * p.Hkv, p.T, D / 8);
-  p.chunks = l.chunks;
   if (l.rows_per_thread == 4)
     cache_write_kernel<FMT, D, T, 4><<<l.blocks, l.threads, 0, stream>>>(p);
   else
@@ -259,7 +256,6 @@ int write_t(WriteParams p, cudaStream_t stream) {
 template <int FMT, int D, typename T>
 int read_t(ReadParams p, cudaStream_t stream) {
   const Launch l = plan_launch(2u * p.B * p.Hkv, p.T, D * (int)sizeof(T) / 16);
-  p.chunks = l.chunks;
   if (l.rows_per_thread == 4)
     cache_read_kernel<FMT, D, T, 4><<<l.blocks, l.threads, 0, stream>>>(p);
   else

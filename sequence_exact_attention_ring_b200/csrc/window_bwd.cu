@@ -5,16 +5,21 @@
 // that see each other:
 //     P = exp(scale q k^T - lse),  dV = P^T dO,  dP = dO V^T,  Delta = rowsum(dO * O),
 //     dS = P * (dP - Delta),  dQ = scale dS K,  dK = scale dS^T Q
-// (dK, dV summed over the query heads of a group). P and dS are rounded to bf16 for their
-// products; sums and statistics are fp32.
+// (dK, dV summed over the query heads of a group). P and dS are rounded to bf16 for the
+// products that give dV and dK; sums and statistics are fp32. For dQ, dS enters as two bf16
+// terms, its rounding and what that left: a row of dS sums to about zero, so that dQ is small
+// against its terms and their rounding would show (1.5 to 1.6 times the error of rounding
+// the result alone; with two terms 1.0).
 //
 // Kernels, on one stream:
 //   prep    Delta and lse log2 e per row, padded to whole 128-row tiles (+inf / 0)
-//   dkdv    one CTA per 128-key tile and part of its queries: 64 query rows at a time,
+//   grads   CTAs of two kinds, in one launch: the short ones fill the SMs that the last of
+//           the long ones leave idle.
+//           dkdv: a 128-key tile and part of its queries, 64 query rows at a time,
 //           S^T = K Q^T and dP^T = V dO^T into tensor memory, P^T and dS^T by eight warps,
 //           then dV += P^T dO and dK += dS^T Q with the packed operand in tensor memory
+//           dq: 128 query rows, 64 keys at a time: S, dP, dS, dQ += dS K
 //   reduce  sums the parts of tiles that have more than one, in a fixed order
-//   dq      one CTA per 128 query rows, 64 keys at a time: S, dP, dS, dQ += dS K
 // as in the ring's backward kernels (bwd_sm100.cu), from which the tensor-memory layout,
 // the double buffering and the one-slot-per-step rings are taken over. No atomics: the
 // same call gives the same bits.
@@ -125,8 +130,9 @@ struct Params {
   const float* lse2;   // [B*Hq][s_pad]
   const float* delta;
   int64_t s_pad;
-  void* out0;          // dK or dQ
-  void* out1;          // dV
+  void* dq;
+  void* dk;
+  void* dv;
   float* parts;        // [part][dV, dK][128][D]
   float scale, scale_log2;
   int* status;
@@ -199,7 +205,8 @@ __host__ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int c0) 
 
 // P and dS of 32 columns from the raw scores and dP, packed to bf16 pairs: P = 2^x with
 // x = s scale_log2 - lse2, dS = P (dP - Delta). kPerCol: the statistics belong to the
-// columns. Columns whose bit is 0 give zeros whatever they held.
+// columns, and pp receives P; otherwise it receives what the rounding of dS left (exact in
+// fp32, rounded to bf16). Columns whose bit is 0 give zeros whatever they held.
 template <bool kPerCol>
 __device__ __forceinline__ void p_ds_chunk(const uint32_t (&s)[32], const uint32_t (&dp)[32], const float* lse2c,
                                            const float* deltac, float row_lse2, float row_delta, float scale_log2,
@@ -227,8 +234,13 @@ __device__ __forceinline__ void p_ds_chunk(const uint32_t (&s)[32], const uint32
       if (!(see >> e & 1)) p0 = d0 = 0.f;
       if (!(see >> (e + 1) & 1)) p1 = d1 = 0.f;
     }
-    pp[e / 2] = pack_bf16x2(p0, p1);
     pds[e / 2] = pack_bf16x2(d0, d1);
+    if (kPerCol) {
+      pp[e / 2] = pack_bf16x2(p0, p1);
+    } else {
+      const uint32_t r = pds[e / 2];
+      pp[e / 2] = pack_bf16x2(d0 - __uint_as_float(r << 16), d1 - __uint_as_float(r & 0xffff0000u));
+    }
   }
 }
 
@@ -269,13 +281,9 @@ __global__ void __launch_bounds__(256) window_prep_kernel(const uint16_t* __rest
 
 // ------------------------------------------------------------------------------ dK, dV
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    window_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const Params p) {
+__device__ __forceinline__ void dkdv_unit(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtensorMap& tm_k,
+                                          const CUtensorMap& tm_v, const Params& p, uint8_t* smem, int64_t unit) {
   using C = CfgA<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
@@ -306,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Watchdog wd{abort_flag, p.status, p.watchdog_ns};
-  const KeyUnit U = key_unit(g, p.plan, blockIdx.x);
+  const KeyUnit U = key_unit(g, p.plan, unit);
   const int rep = g.Hq / g.Hkv;
   const int per_head = (int)(U.s1 - U.s0);
   const int N = (U.h1 - U.h0) * per_head;  // steps
@@ -442,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (U.part < 0) {
         const bool row_ok = u < g.S;
         const int64_t out_row = U.bh * g.S + (row_ok ? u : 0);
-        store_row_cols<D / 2>(tAcc, N > 0, row_ok, 1.f, false, p.out1, out_row, D, hh * (D / 2));
-        store_row_cols<D / 2>(tAcc + D, N > 0, row_ok, p.scale, false, p.out0, out_row, D, hh * (D / 2));
+        store_row_cols<D / 2>(tAcc, N > 0, row_ok, 1.f, false, p.dv, out_row, D, hh * (D / 2));
+        store_row_cols<D / 2>(tAcc + D, N > 0, row_ok, p.scale, false, p.dk, out_row, D, hh * (D / 2));
       } else {
         store_row_cols<D / 2>(tAcc, N > 0, true, 1.f, true, p.parts, U.part * 2 * BT + r, D, hh * (D / 2));
         store_row_cols<D / 2>(tAcc + D, N > 0, true, p.scale, true, p.parts, U.part * 2 * BT + BT + r, D, hh * (D / 2));
@@ -459,13 +467,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Sums a tile's parts, first to last. One thread per 8 columns of a key row of dV or dK.
-// Covers the sink tiles (pick = 0) or the others (pick = 1).
+// Sums a tile's parts, first to last. One thread per 8 columns of a key row of dV or dK; the
+// first `sink_items` threads take the sink tiles, the others the tiles behind them.
 template <int D>
-__global__ void __launch_bounds__(256) window_reduce_kernel(const Params p, int pick, int64_t items) {
-  const int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(256) window_reduce_kernel(const __grid_constant__ Params p, int64_t sink_items,
+                                                            int64_t items) {
+  int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (it >= items) return;
   const Plan& pl = p.plan;
+  const bool sink = it < sink_items;
+  if (!sink) it -= sink_items;
   constexpr int kTpr = D / 8;
   const int c = (int)(it % kTpr) * 8;
   int64_t x = it / kTpr;
@@ -473,34 +484,32 @@ __global__ void __launch_bounds__(256) window_reduce_kernel(const Params p, int 
   x /= BT;
   const int which = (int)(x % 2);  // 0 dV, 1 dK
   x /= 2;
-  const int64_t tiles = pick == 0 ? pl.sink_tiles : pl.tiles - pl.sink_tiles;
+  const int64_t tiles = sink ? pl.sink_tiles : pl.tiles - pl.sink_tiles;
   const int64_t t = x % tiles, bh = x / tiles;
-  const int64_t u = (t + (pick == 0 ? 0 : pl.sink_tiles)) * BT + r;
+  const int64_t u = (t + (sink ? 0 : pl.sink_tiles)) * BT + r;
   if (u >= p.g.S) return;
-  const int n = pick == 0 ? pl.segs * pl.splits : pl.splits;
-  const int64_t first = (pick == 0 ? 0 : (pl.segs * pl.splits > 1 ? pl.sink_units : 0)) + (bh * tiles + t) * n;
+  const int n = sink ? pl.segs * pl.splits : pl.splits;
+  const int64_t first = (sink ? 0 : (pl.segs * pl.splits > 1 ? pl.sink_units : 0)) + (bh * tiles + t) * n;
   float acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
   const float* src = p.parts + ((first * 2 + which) * BT + r) * D + c;
+#pragma unroll 4
   for (int i = 0; i < n; ++i, src += 2 * BT * D) {
     const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
     acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
     acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
   }
-  uint16_t* dst = static_cast<uint16_t*>(which ? p.out0 : p.out1) + (bh * p.g.S + u) * D + c;
+  uint16_t* dst = static_cast<uint16_t*>(which ? p.dk : p.dv) + (bh * p.g.S + u) * D + c;
   *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
                                               pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
 }
 
 // ---------------------------------------------------------------------------------- dQ
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    window_dq_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const Params p) {
+__device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p,
+                                        uint8_t* smem, int64_t u) {
   using C = CfgB<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
@@ -534,7 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // units: the heads of a group innermost (shared K and V), then the row blocks
   const int rep = g.Hq / g.Hkv;
   const int64_t blocks = p.s_pad / BT;
-  int64_t u = blockIdx.x;
   const int hr = (int)(u % rep);
   u /= rep;
   const int64_t a0 = (u % blocks) * BT;
@@ -599,10 +607,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint64_t mk = smem_desc_sw128(slot_addr(n), kStepBoxBytes, 1024);
 #pragma unroll
-      for (int k = 0; k < TS / 16; ++k)  // dQ += dS K
-        if (issuer)
+      for (int k = 0; k < TS / 16; ++k)  // dQ += dS K, both terms of dS
+        if (issuer) {
           mma_ts(tmem + kColAcc, tmem + col_s(b) + packed_step_col(k), mnmajor_step(mk, k), C::kIdescTS,
                  !(n == 0 && k == 0));
+          mma_ts(tmem + kColAcc, tmem + col_dp(b) + packed_step_col(k), mnmajor_step(mk, k), C::kIdescTS, 1);
+        }
       if (issuer) mma_commit(&empty[slot_of(n)]);
       if (n + 2 < N && !(ok = issue_sd(n + 2))) break;
     }
@@ -658,8 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(tmem + lane_off + col_s(b) + 32 * hh, sv);
       tmem_ld32(tmem + lane_off + col_dp(b) + 32 * hh, dpv);
       tmem_wait_ld();
+      // only dS feeds the dQ product: its rounding to bf16 and the rounding of the rest
       p_ds_chunk<false>(sv, dpv, nullptr, nullptr, row_lse2, row_delta, p.scale_log2, see, pp, pds);
-      tmem_st16(tmem + lane_off + col_s(b) + 32 * hh, pds);  // only dS feeds the dQ product
+      tmem_st16(tmem + lane_off + col_s(b) + 32 * hh, pds);
+      tmem_st16(tmem + lane_off + col_dp(b) + 32 * hh, pp);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -668,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (N > 0 && ok && mbar_wait(&bars[kB_Done], 0, wd)) {
       tc_fence_after();
       const int64_t out_row = (int64_t)bh_q * g.S + (row_ok ? a : 0);
-      store_row_cols<D / 2>(tmem + lane_off + kColAcc + hh * (D / 2), true, row_ok, p.scale, false, p.out0, out_row, D,
+      store_row_cols<D / 2>(tmem + lane_off + kColAcc + hh * (D / 2), true, row_ok, p.scale, false, p.dq, out_row, D,
                             hh * (D / 2));
     }
   }
@@ -679,6 +691,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_grads_kernel(const __grid_constant__ CUtensorMap tm_q64, const __grid_constant__ CUtensorMap tm_do64,
+                        const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_k64, const __grid_constant__ CUtensorMap tm_v64,
+                        const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (blockIdx.x < p.plan.units)
+    dkdv_unit<D>(tm_q64, tm_do64, tm_k, tm_v, p, smem, blockIdx.x);
+  else
+    dq_unit<D>(tm_k64, tm_v64, p, smem, blockIdx.x - p.plan.units);
 }
 
 Plan make_plan(const WinGeom& g) {
@@ -733,7 +759,7 @@ int launch(const void* q, const void* k, const void* v, const void* out, const f
   p.watchdog_ns = watchdog_ns;
   const int64_t prep_blocks = (rows + 256 / (D / 8) - 1) / (256 / (D / 8));
   const int64_t q_units = (int64_t)g.B * g.Hq * (p.s_pad / BT);
-  if (prep_blocks > 0x7fffffff || p.plan.units > 0x7fffffff || q_units > 0x7fffffff) return RING_ATTN_EINVAL;
+  if (prep_blocks > 0x7fffffff || p.plan.units + q_units > 0x7fffffff) return RING_ATTN_EINVAL;
   CUtensorMap mq, mdo, mk, mv, mk64, mv64;
   int rc;
   const int64_t bhq = (int64_t)g.B * g.Hq, bhk = (int64_t)g.B * g.Hkv;
@@ -743,31 +769,24 @@ int launch(const void* q, const void* k, const void* v, const void* out, const f
   if ((rc = encode_rows_map(&mv, v, bhk, g.S, D, BT)) != 0) return rc;
   if ((rc = encode_rows_map(&mk64, k, bhk, g.S, D, TS)) != 0) return rc;
   if ((rc = encode_rows_map(&mv64, v, bhk, g.S, D, TS)) != 0) return rc;
-  if (cudaFuncSetAttribute(window_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgA<D>::kSmemBytes) !=
-          cudaSuccess ||
-      cudaFuncSetAttribute(window_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CfgB<D>::kSmemBytes) !=
-          cudaSuccess)
+  constexpr int smem = CfgA<D>::kSmemBytes > CfgB<D>::kSmemBytes ? CfgA<D>::kSmemBytes : CfgB<D>::kSmemBytes;
+  if (cudaFuncSetAttribute(window_grads_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return RING_ATTN_ECUDA;
   window_prep_kernel<D><<<(unsigned)prep_blocks, 256, 0, stream>>>(
       static_cast<const uint16_t*>(out), static_cast<const uint16_t*>(dout), lse, scratch, scratch + rows, g.S, p.s_pad,
       rows, status);
   if (cudaGetLastError() != cudaSuccess) return RING_ATTN_ECUDA;
-  p.out0 = dk;
-  p.out1 = dv;
-  window_dkdv_kernel<D><<<(unsigned)p.plan.units, kThreads, CfgA<D>::kSmemBytes, stream>>>(mq, mdo, mk, mv, p);
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  window_grads_kernel<D><<<(unsigned)(p.plan.units + q_units), kThreads, smem, stream>>>(mq, mdo, mk, mv, mk64, mv64, p);
   if (cudaGetLastError() != cudaSuccess) return RING_ATTN_ECUDA;
-  for (int pick = 0; pick < 2; ++pick) {
-    const int n = pick == 0 ? p.plan.segs * p.plan.splits : p.plan.splits;
-    const int64_t tiles = pick == 0 ? p.plan.sink_tiles : p.plan.tiles - p.plan.sink_tiles;
-    const int64_t items = bhk * tiles * 2 * BT * (D / 8);
-    if (n == 1 || items == 0) continue;
-    if ((items + 255) / 256 > 0x7fffffff) return RING_ATTN_EINVAL;
-    window_reduce_kernel<D><<<(unsigned)((items + 255) / 256), 256, 0, stream>>>(p, pick, items);
-    if (cudaGetLastError() != cudaSuccess) return RING_ATTN_ECUDA;
-  }
-  p.out0 = dq;
-  p.out1 = nullptr;
-  window_dq_kernel<D><<<(unsigned)q_units, kThreads, CfgB<D>::kSmemBytes, stream>>>(mk64, mv64, p);
+  const int64_t per_tile = bhk * 2 * BT * (D / 8);
+  const int64_t sink_items = p.plan.segs * p.plan.splits > 1 ? per_tile * p.plan.sink_tiles : 0;
+  const int64_t items = sink_items + (p.plan.splits > 1 ? per_tile * (p.plan.tiles - p.plan.sink_tiles) : 0);
+  if (items == 0) return RING_ATTN_OK;
+  if ((items + 255) / 256 > 0x7fffffff) return RING_ATTN_EINVAL;
+  window_reduce_kernel<D><<<(unsigned)((items + 255) / 256), 256, 0, stream>>>(p, sink_items, items);
   return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
 }
 
