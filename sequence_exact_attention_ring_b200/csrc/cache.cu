@@ -43,20 +43,55 @@ struct ReadParams {
   int64_t capacity;
 };
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// Eight consecutive elements of a row as they were loaded; `amax` gives the largest
+// magnitude as fp32 bits (an unsigned maximum, so a NaN is kept), `scaled` the values times
+// a power of two. bf16 is worked on in pairs: its exponents are fp32's, so the product by a
+// power of two is exact but for values that end below every code's half step.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
   }
-}
+  __device__ __forceinline__ uint32_t amax() const {
+    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+    return m;
+  }
+  __device__ __forceinline__ void scaled(float f, float (&y)[8]) const {
+    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = x[e] * f;
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void clear() { w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ uint32_t amax() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+  }
+  __device__ __forceinline__ void scaled(float f, float (&y)[8]) const {
+    const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]), f2);
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(&h);
+      y[2 * i] = __uint_as_float(v << 16);
+      y[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
+    }
+  }
+};
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -98,14 +133,13 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
   uint8_t* codes = w ? p.codes[1] : p.codes[0];
   uint8_t* scale = w ? p.scale[1] : p.scale[0];
   if (n > p.T && p.status && threadIdx.x == 0) atomicExch(p.status, RING_ATTN_EINVAL);
-  float x[kRows][8];
+  Eight<T> x[kRows];
   int64_t dst[kRows];
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     const uint32_t i = run.first + u * rpb + threadIdx.x / kTpr;
     dst[u] = -1;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
+    x[u].clear();
     if (i >= (uint32_t)p.T || (int32_t)i >= n) continue;
     const int64_t pos = start + i;
     const int64_t from = p.index ? (int64_t)p.index[(int64_t)run.b * p.T + i] : (int64_t)i;
@@ -113,45 +147,40 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
       if (p.status && sub == 0) atomicExch(p.status, RING_ATTN_EINVAL);
       continue;
     }
-    load8(src + from * stride, x[u]);
+    x[u].load(src + from * stride);
     dst[u] = head_row + pos;
   }
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
+    float y[8];
     if (FMT == RING_ATTN_CACHE_BF16) {
       if (dst[u] < 0) continue;
       uint4 o;
-      o.x = bf16_pair(x[u][0], x[u][1]);
-      o.y = bf16_pair(x[u][2], x[u][3]);
-      o.z = bf16_pair(x[u][4], x[u][5]);
-      o.w = bf16_pair(x[u][6], x[u][7]);
+      if constexpr (sizeof(T) == 2) {
+        o = x[u].w;
+      } else {
+        x[u].scaled(1.f, y);
+        o = make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(y[4], y[5]), bf16_pair(y[6], y[7]));
+      }
       *reinterpret_cast<uint4*>(codes + dst[u] * (2 * D) + sub * 16) = o;
       continue;
     }
-    // the block's largest magnitude as fp32 bits: an unsigned maximum, so a NaN is kept
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t a = __float_as_uint(x[u][e]) & 0x7fffffffu;
-      m = a > m ? a : m;
-    }
+    uint32_t m = x[u].amax();
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     if (dst[u] < 0) continue;
     const uint32_t byte = mx_scale_byte<FMT>(m);
-    const float inv = byte == 255u ? 0.f : mx_inverse_scale(byte);
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = byte == 255u ? 0.f : x[u][e] * inv;
+    const bool finite = byte != 255u;  // the codes of a block that is not finite are zeros
+    x[u].scaled(mx_inverse_scale(byte), y);
     if (FMT == RING_ATTN_CACHE_MXFP8) {
       uint2 o;
       o.x = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
       o.y = e4m3_pair(y[4], y[5]) | (e4m3_pair(y[6], y[7]) << 16);
-      *reinterpret_cast<uint2*>(codes + dst[u] * D + sub * 8) = o;
+      *reinterpret_cast<uint2*>(codes + dst[u] * D + sub * 8) = finite ? o : make_uint2(0u, 0u);
     } else {
       const uint32_t o = e2m1_pair(y[0], y[1]) | (e2m1_pair(y[2], y[3]) << 8) | (e2m1_pair(y[4], y[5]) << 16) |
                          (e2m1_pair(y[6], y[7]) << 24);
-      *reinterpret_cast<uint32_t*>(codes + dst[u] * (D / 2) + sub * 4) = o;
+      *reinterpret_cast<uint32_t*>(codes + dst[u] * (D / 2) + sub * 4) = finite ? o : 0u;
     }
     if (sub % 4 == 0) scale[dst[u] * (D / kMxBlock) + sub / 4] = (uint8_t)byte;
   }
