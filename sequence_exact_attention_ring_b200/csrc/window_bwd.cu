@@ -12,7 +12,7 @@
 // the result alone; with two terms 1.0).
 //
 // Kernels, on one stream:
-//   prep    Delta and lse log2 e per row, padded to whole 128-row tiles (+inf / 0)
+//   prep    -Delta and -lse log2 e per row, padded to whole 128-row tiles (0 / -inf)
 //   grads   CTAs of two kinds, in one launch: the short ones fill the SMs that the last of
 //           the long ones leave idle.
 //           dkdv: a 128-key tile and part of its queries, 64 query rows at a time,
@@ -127,8 +127,8 @@ struct Params {
   Plan plan;
   const uint16_t* q;
   const uint16_t* dout;
-  const float* lse2;   // [B*Hq][s_pad]
-  const float* delta;
+  const float* nlse2;  // [B*Hq][s_pad]: -lse log2 e
+  const float* ndelta; // -Delta
   int64_t s_pad;
   void* dq;
   void* dk;
@@ -188,6 +188,20 @@ __host__ __device__ __forceinline__ KeyUnit key_unit(const WinGeom& g, const Pla
   return x;
 }
 
+// Slot and phase of a ring's step, counted along (a division per step would stand in the
+// issuing thread's way).
+template <int kSlots>
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kSlots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity)) {
@@ -203,44 +217,88 @@ __host__ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int c0) 
   return (0xffffffffu >> (32 - (hi - lo))) << lo;
 }
 
-// P and dS of 32 columns from the raw scores and dP, packed to bf16 pairs: P = 2^x with
-// x = s scale_log2 - lse2, dS = P (dP - Delta). kPerCol: the statistics belong to the
-// columns, and pp receives P; otherwise it receives what the rounding of dS left (exact in
-// fp32, rounded to bf16). Columns whose bit is 0 give zeros whatever they held.
-template <bool kPerCol>
-__device__ __forceinline__ void p_ds_chunk(const uint32_t (&s)[32], const uint32_t (&dp)[32], const float* lse2c,
-                                           const float* deltac, float row_lse2, float row_delta, float scale_log2,
-                                           uint32_t see, uint32_t* pp, uint32_t* pds) {
+// Queries [u, key_past) see key u.
+__host__ __device__ __forceinline__ int64_t key_past(const WinGeom& g, int64_t u) {
+  return u < g.sinks || u + g.window > g.S ? g.S : u + g.window;
+}
+// Steps whose every query sees every key of tile kt: [in0, in1), most of a tile's.
+__host__ __device__ __forceinline__ void inner_steps(const WinGeom& g, int64_t kt, int64_t& in0, int64_t& in1) {
+  in0 = (kt + 1) * (BT / TS);
+  in1 = ((kt + 1) * BT <= g.sinks ? g.S : key_past(g, kt * BT < g.sinks ? g.sinks : kt * BT)) / TS;
+}
+// Queries of 32 columns of step s that see key u.
+__host__ __device__ __forceinline__ uint32_t key_sees(int64_t u, int64_t past, int64_t s, int c0, int64_t in0,
+                                                      int64_t in1) {
+  if (s >= in0 && s < in1) return 0xffffffffu;
+  return range_bits(win_clip(u - s * TS, TS), win_clip(past - s * TS, TS), c0);
+}
+// Keys of 32 columns of the step that starts at key `first` that query a of the block at a0 sees.
+__host__ __device__ __forceinline__ uint32_t query_sees(const WinGeom& g, int64_t a0, int64_t a, int64_t first, int c0) {
+  if (first + TS - 1 <= a0 && first > a0 + BT - 1 - g.window) return 0xffffffffu;
+  const WinCut cut = win_cut(g, a, first, TS);
+  return range_bits(cut.lo, cut.hi, c0) | range_bits(0, cut.sk < cut.hi ? cut.sk : cut.hi, c0);
+}
+
+// Raw scores and dP of two neighbouring columns to P and dS: P = 2^x with x = s scale_log2 -
+// lse2, dS = P (dP - Delta); the statistics come negated.
+__device__ __forceinline__ void p_ds_pair(uint32_t s0, uint32_t s1, uint32_t dp0, uint32_t dp1, uint64_t c2, uint64_t nl,
+                                          uint64_t nd, float& p0, float& p1, float& d0, float& d1) {
+  float x0, x1;
+  f2_unpack(f2_fma(f2_pack(s0, s1), c2, nl), x0, x1);
+  p0 = ex2_approx(x0);
+  p1 = ex2_approx(x1);
+  f2_unpack(f2_mul(f2_pack(__float_as_uint(p0), __float_as_uint(p1)), f2_add(f2_pack(dp0, dp1), nd)), d0, d1);
+}
+
+// dkdv: 32 keys x 32 queries of a warp as two fragments of 16 keys (tmem_ld_frag16), so that a
+// thread needs the statistics of 8 queries for its 32 pairs and not of 32: they come from
+// shared memory, whose reads by the products bound the step (with a key per thread, 64 values
+// read by each, a step took 1780 cycles; 1280 are the products'). nlse2c, ndeltac: those of
+// the thread's first query. see[2 t + j]: the queries from there on that see its key of
+// fragment t, row j; zeros for the others whatever they held.
+template <bool kWhole>
+__device__ __forceinline__ void p_ds_keys(const uint32_t (&s)[32], const uint32_t (&dp)[32], const float* nlse2c,
+                                          const float* ndeltac, float scale_log2, const uint32_t (&see)[4],
+                                          uint32_t (&pp)[16], uint32_t (&pds)[16]) {
   const uint64_t c2 = f2_splat(scale_log2);
-  const uint64_t l2r = f2_splat(row_lse2);
-  const uint64_t dlr = f2_splat(row_delta);
-  const bool whole = see == 0xffffffffu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 lv = *reinterpret_cast<const float2*>(nlse2c + 8 * i);
+    const float2 dv = *reinterpret_cast<const float2*>(ndeltac + 8 * i);
+    const uint64_t nl = f2_pack(__float_as_uint(lv.x), __float_as_uint(lv.y));
+    const uint64_t nd = f2_pack(__float_as_uint(dv.x), __float_as_uint(dv.y));
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int e = (x / 2) * 16 + 4 * i + 2 * (x % 2), o = (x / 2) * 8 + 2 * i + x % 2;
+      float p0, p1, d0, d1;
+      p_ds_pair(s[e], s[e + 1], dp[e], dp[e + 1], c2, nl, nd, p0, p1, d0, d1);
+      if (!kWhole) {
+        if (!(see[x] >> (8 * i) & 1)) p0 = d0 = 0.f;
+        if (!(see[x] >> (8 * i + 1) & 1)) p1 = d1 = 0.f;
+      }
+      pp[o] = pack_bf16x2(p0, p1);
+      pds[o] = pack_bf16x2(d0, d1);
+    }
+  }
+}
+
+// dq: 32 columns of a query, its statistics in registers; pds receives dS, rest what its
+// rounding left (exact in fp32, rounded to bf16).
+template <bool kWhole>
+__device__ __forceinline__ void ds_query(const uint32_t (&s)[32], const uint32_t (&dp)[32], float nlse2, float ndelta,
+                                         float scale_log2, uint32_t see, uint32_t (&pds)[16], uint32_t (&rest)[16]) {
+  const uint64_t c2 = f2_splat(scale_log2), nl = f2_splat(nlse2), nd = f2_splat(ndelta);
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
-    uint64_t l2 = l2r, dl = dlr;
-    if (kPerCol) {
-      const float2 lv = *reinterpret_cast<const float2*>(lse2c + e);
-      const float2 dv = *reinterpret_cast<const float2*>(deltac + e);
-      l2 = f2_pack(__float_as_uint(lv.x), __float_as_uint(lv.y));
-      dl = f2_pack(__float_as_uint(dv.x), __float_as_uint(dv.y));
+    float p0, p1, d0, d1;
+    p_ds_pair(s[e], s[e + 1], dp[e], dp[e + 1], c2, nl, nd, p0, p1, d0, d1);
+    if (!kWhole) {
+      if (!(see >> e & 1)) d0 = 0.f;
+      if (!(see >> (e + 1) & 1)) d1 = 0.f;
     }
-    float x0, x1;
-    f2_unpack(f2_sub(f2_mul(f2_pack(s[e], s[e + 1]), c2), l2), x0, x1);
-    float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-    const uint64_t df = f2_sub(f2_pack(dp[e], dp[e + 1]), dl);
-    float d0, d1;
-    f2_unpack(f2_mul(f2_pack(__float_as_uint(p0), __float_as_uint(p1)), df), d0, d1);
-    if (!whole) {
-      if (!(see >> e & 1)) p0 = d0 = 0.f;
-      if (!(see >> (e + 1) & 1)) p1 = d1 = 0.f;
-    }
-    pds[e / 2] = pack_bf16x2(d0, d1);
-    if (kPerCol) {
-      pp[e / 2] = pack_bf16x2(p0, p1);
-    } else {
-      const uint32_t r = pds[e / 2];
-      pp[e / 2] = pack_bf16x2(d0 - __uint_as_float(r << 16), d1 - __uint_as_float(r & 0xffff0000u));
-    }
+    const uint32_t r = pack_bf16x2(d0, d1);
+    pds[e / 2] = r;
+    rest[e / 2] = pack_bf16x2(d0 - __uint_as_float(r << 16), d1 - __uint_as_float(r & 0xffff0000u));
   }
 }
 
@@ -249,8 +307,8 @@ __device__ __forceinline__ void p_ds_chunk(const uint32_t (&s)[32], const uint32
 template <int D>
 __global__ void __launch_bounds__(256) window_prep_kernel(const uint16_t* __restrict__ out,
                                                           const uint16_t* __restrict__ dout,
-                                                          const float* __restrict__ lse, float* __restrict__ lse2,
-                                                          float* __restrict__ delta, int64_t S, int64_t s_pad,
+                                                          const float* __restrict__ lse, float* __restrict__ nlse2,
+                                                          float* __restrict__ ndelta, int64_t S, int64_t s_pad,
                                                           int64_t rows, int* status) {
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = RING_ATTN_OK;
   constexpr int kTpr = D / 8;
@@ -274,8 +332,8 @@ __global__ void __launch_bounds__(256) window_prep_kernel(const uint16_t* __rest
 #pragma unroll
   for (int off = kTpr / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
   if (in && sub == 0) {
-    lse2[row] = real ? lse[bh * S + a] * 1.4426950408889634f : INFINITY;
-    delta[row] = acc;
+    nlse2[row] = real ? lse[bh * S + a] * -1.4426950408889634f : -INFINITY;
+    ndelta[row] = -acc;
   }
 }
 
@@ -345,8 +403,8 @@ __device__ __forceinline__ void dkdv_unit(const CUtensorMap& tm_q, const CUtenso
           for (int bx = 0; bx < D / BOXW; ++bx)
             tma_load_4d(dst + C::kSlotDO + bx * kStepBoxBytes, &tm_do, &full[slot], bx * BOXW, (int)(s * TS), 0, bh_q);
           const int64_t stat = (int64_t)bh_q * p.s_pad + s * TS;
-          bulk_load(dst + C::kSlotLse, p.lse2 + stat, kStepStatBytes, &full[slot]);
-          bulk_load(dst + C::kSlotDelta, p.delta + stat, kStepStatBytes, &full[slot]);
+          bulk_load(dst + C::kSlotLse, p.nlse2 + stat, kStepStatBytes, &full[slot]);
+          bulk_load(dst + C::kSlotDelta, p.ndelta + stat, kStepStatBytes, &full[slot]);
         }
       }
       if (!ok) {
@@ -357,65 +415,65 @@ __device__ __forceinline__ void dkdv_unit(const CUtensorMap& tm_q, const CUtenso
       }
     }
   } else if (warp == kMmaWarp) {
-    const bool issuer = elect_one_sync();
-    const uint32_t sbase = smem_u32(smem);
-    const uint64_t dK = smem_desc_sw128(sbase, 0, 1024);
-    const uint64_t dV = smem_desc_sw128(sbase + C::kOffV, 0, 1024);
-    auto all = [&](bool r) { return __all_sync(0xffffffffu, r) != 0; };
-    auto slot_addr = [&](int n) { return sbase + C::kOffRing + slot_of(n) * C::kSlotBytes; };
-    auto issue_st = [&](int n) -> bool {
-      if (!all(mbar_wait(&full[slot_of(n)], phase_of(n), wd))) return false;
-      tc_fence_after();
-      const int b = n & 1;
-      const uint64_t bq = smem_desc_sw128(slot_addr(n), 0, 1024);
-      const uint64_t bd = smem_desc_sw128(slot_addr(n) + C::kSlotDO, 0, 1024);
+    // one thread waits and issues: the tensor pipe holds two or three products ahead, so what
+    // passes between a step's last and the next one's first is time that it idles
+    if (elect_one_sync()) {
+      const uint32_t sbase = smem_u32(smem);
+      const uint64_t dK = smem_desc_sw128(sbase, 0, 1024);
+      const uint64_t dV = smem_desc_sw128(sbase + C::kOffV, 0, 1024);
+      RingPos<C::kSlots> in, use;  // steps of the next S^T and of the next dV
+      auto issue_st = [&](int b) -> bool {
+        if (!mbar_wait(&full[in.slot], in.phase, wd)) return false;
+        tc_fence_after();
+        const uint32_t at = sbase + C::kOffRing + in.slot * C::kSlotBytes;
+        const uint64_t bq = smem_desc_sw128(at, 0, 1024);
+        const uint64_t bd = smem_desc_sw128(at + C::kSlotDO, 0, 1024);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        if (issuer)
+        for (int k = 0; k < D / 16; ++k)
           mma_ss(tmem + col_s(b), kmajor_step<kBoxBytes>(dK, k), kmajor_step<kStepBoxBytes>(bq, k), kIdescSS, k > 0);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        if (issuer)
+        for (int k = 0; k < D / 16; ++k)
           mma_ss(tmem + col_dp(b), kmajor_step<kBoxBytes>(dV, k), kmajor_step<kStepBoxBytes>(bd, k), kIdescSS, k > 0);
-      if (issuer) mma_commit(&bars[kA_STFull + b]);
-      return true;
-    };
-    bool ok = N > 0 && all(mbar_wait(&bars[kA_KVFull], 0, wd));
-    if (ok) ok = issue_st(0);
-    if (ok && N > 1) ok = issue_st(1);
-    for (int n = 0; ok && n < N; ++n) {
-      const int b = n & 1;
-      if (!(ok = all(mbar_wait(&bars[kA_PReady + b], (uint32_t)((n >> 1) & 1), wd)))) break;
-      tc_fence_after();
-      const uint64_t mq = smem_desc_sw128(slot_addr(n), kStepBoxBytes, 1024);
-      const uint64_t md = smem_desc_sw128(slot_addr(n) + C::kSlotDO, kStepBoxBytes, 1024);
+        mma_commit(&bars[kA_STFull + b]);
+        in.next();
+        return true;
+      };
+      bool ok = N > 0 && mbar_wait(&bars[kA_KVFull], 0, wd);
+      if (ok) ok = issue_st(0);
+      if (ok && N > 1) ok = issue_st(1);
+      for (int n = 0; ok && n < N; ++n, use.next()) {
+        const int b = n & 1;
+        const uint32_t at = sbase + C::kOffRing + use.slot * C::kSlotBytes;
+        const uint64_t mq = smem_desc_sw128(at, kStepBoxBytes, 1024);
+        const uint64_t md = smem_desc_sw128(at + C::kSlotDO, kStepBoxBytes, 1024);
+        if (!(ok = mbar_wait(&bars[kA_PReady + b], (uint32_t)((n >> 1) & 1), wd))) break;
+        tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < TS / 16; ++k)  // dV += P^T dO
-        if (issuer)
+        for (int k = 0; k < TS / 16; ++k)  // dV += P^T dO
           mma_ts(tmem + kColAcc, tmem + col_s(b) + packed_step_col(k), mnmajor_step(md, k), C::kIdescTS,
                  !(n == 0 && k == 0));
 #pragma unroll
-      for (int k = 0; k < TS / 16; ++k)  // dK += dS^T Q
-        if (issuer)
+        for (int k = 0; k < TS / 16; ++k)  // dK += dS^T Q
           mma_ts(tmem + kColAcc + D, tmem + col_dp(b) + packed_step_col(k), mnmajor_step(mq, k), C::kIdescTS,
                  !(n == 0 && k == 0));
-      if (issuer) mma_commit(&empty[slot_of(n)]);
-      // buffer b is free for step n + 2 once these products have read its P and dS
-      if (n + 2 < N && !(ok = issue_st(n + 2))) break;
-    }
-    if (issuer) {
+        mma_commit(&empty[use.slot]);
+        // buffer b is free for step n + 2 once these products have read its P and dS
+        if (n + 2 < N && !(ok = issue_st(b))) break;
+      }
       mma_commit(&bars[kA_Done]);
       mma_commit(&bars[kA_Drain]);
+      drain_wait(&bars[kA_Drain], 0, p.watchdog_ns);
     }
-    drain_wait(&bars[kA_Drain], 0, p.watchdog_ns);
+    __syncwarp();
   } else if (warp < kEwWarps) {
     // warp = 4 hh + wq: TMEM lanes 32 wq (key rows), query columns 32 hh .. 32 hh + 31 of a step
     const int wq = warp % 4, hh = warp / 4;
     const int r = wq * 32 + lane;
     const int64_t u = U.kt * BT + r;  // this thread's key
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    // queries [u, past) see it
-    const int64_t past = u < g.sinks || u + g.window > g.S ? g.S : u + g.window;
+    const int fr = lane / 4, fc = 2 * (lane % 4);  // fragment row, first column
+    int64_t in0, in1;
+    inner_steps(g, U.kt, in0, in1);
     bool ok = true;
     int n = 0;
     for (int h = U.h0; h < U.h1 && ok; ++h) {
@@ -426,17 +484,36 @@ __device__ __forceinline__ void dkdv_unit(const CUtensorMap& tm_q, const CUtenso
         // the statistics came with the tiles: wait on their barrier too (already complete)
         if (!(ok = mbar_wait(&full[sl], phase_of(n), wd))) break;
         tc_fence_after();
-        const float* lse2c = reinterpret_cast<const float*>(smem + C::kOffRing + sl * C::kSlotBytes + C::kSlotLse);
-        const float* deltac = reinterpret_cast<const float*>(smem + C::kOffRing + sl * C::kSlotBytes + C::kSlotDelta);
-        const uint32_t see = range_bits(win_clip(u - s * TS, TS), win_clip(past - s * TS, TS), 32 * hh);
-        uint32_t sv[32], dpv[32], pp[16], pds[16];
-        tmem_ld32(tmem + lane_off + col_s(b) + 32 * hh, sv);
-        tmem_ld32(tmem + lane_off + col_dp(b) + 32 * hh, dpv);
+        const float* nlse2c = reinterpret_cast<const float*>(smem + C::kOffRing + sl * C::kSlotBytes + C::kSlotLse);
+        const float* ndeltac = reinterpret_cast<const float*>(smem + C::kOffRing + sl * C::kSlotBytes + C::kSlotDelta);
+        nlse2c += 32 * hh + fc;
+        ndeltac += 32 * hh + fc;
+        uint32_t sv[32], dpv[32], pp[16], pds[16], see[4];
+        const uint32_t tS = tmem + lane_off + col_s(b) + 32 * hh, tDP = tmem + lane_off + col_dp(b) + 32 * hh;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          tmem_ld_frag16(tS + (t << 20), sv + 16 * t);
+          tmem_ld_frag16(tDP + (t << 20), dpv + 16 * t);
+        }
+        const bool whole = s >= in0 && s < in1;
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int64_t key = U.kt * BT + wq * 32 + 8 * x + fr;
+            see[x] = key_sees(key, key_past(g, key), s, 32 * hh, in0, in1) >> fc;
+          }
+        }
         tmem_wait_ld();
-        p_ds_chunk<true>(sv, dpv, lse2c + 32 * hh, deltac + 32 * hh, 0.f, 0.f, p.scale_log2, see, pp, pds);
+        if (whole)
+          p_ds_keys<true>(sv, dpv, nlse2c, ndeltac, p.scale_log2, see, pp, pds);
+        else
+          p_ds_keys<false>(sv, dpv, nlse2c, ndeltac, p.scale_log2, see, pp, pds);
         // the packed columns overlap only this warp's own, already loaded fp32 columns
-        tmem_st16(tmem + lane_off + col_s(b) + 32 * hh, pp);
-        tmem_st16(tmem + lane_off + col_dp(b) + 32 * hh, pds);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          tmem_st_frag16(tS + (t << 20), pp + 8 * t);
+          tmem_st_frag16(tDP + (t << 20), pds + 8 * t);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -519,6 +596,41 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorM
   const int lane = threadIdx.x % 32;
   const WinGeom& g = p.g;
 
+  // units: the heads of a group innermost (shared K and V), then the row blocks
+  const int rep = g.Hq / g.Hkv;
+  const int64_t blocks = p.s_pad / BT;
+  const int hr = (int)(u % rep);
+  u /= rep;
+  const int64_t a0 = (u % blocks) * BT;
+  const int bh_kv = (int)(u / blocks);
+  const int bh_q = bh_kv * rep + hr;
+  const WinTiles wt = win_tiles(g, a0, a0 + BT - 1, TS);
+  const int N = win_count(wt);
+  // The elementwise warps' rows of Q and dO, dims (D/2) hh .. as bf16 pairs (the memory order;
+  // rows past the sequence are zeros), and statistics: asked for before all else.
+  uint32_t rows[2][D / 4];
+  float row_nlse2 = 0.f, row_ndelta = 0.f;
+  if (warp < kEwWarps) {
+    const int64_t a = a0 + (warp % 4) * 32 + lane;
+    const bool row_ok = a < g.S;
+    const int64_t base = ((int64_t)bh_q * g.S + (row_ok ? a : 0)) * D + (D / 2) * (warp / 4);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint16_t* src = (t == 0 ? p.q : p.dout) + base;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const uint4 v4 = row_ok ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+        rows[t][4 * c] = v4.x;
+        rows[t][4 * c + 1] = v4.y;
+        rows[t][4 * c + 2] = v4.z;
+        rows[t][4 * c + 3] = v4.w;
+      }
+    }
+    const int64_t stat = (int64_t)bh_q * p.s_pad + a;  // a < s_pad always
+    row_nlse2 = p.nlse2[stat];
+    row_ndelta = p.ndelta[stat];
+  }
+
   if (threadIdx.x == 0) {
     mbar_init(&bars[kB_QReady], kEwWarps);
     for (int b = 0; b < 2; ++b) {
@@ -540,16 +652,6 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorM
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Watchdog wd{abort_flag, p.status, p.watchdog_ns};
-  // units: the heads of a group innermost (shared K and V), then the row blocks
-  const int rep = g.Hq / g.Hkv;
-  const int64_t blocks = p.s_pad / BT;
-  const int hr = (int)(u % rep);
-  u /= rep;
-  const int64_t a0 = (u % blocks) * BT;
-  const int bh_kv = (int)(u / blocks);
-  const int bh_q = bh_kv * rep + hr;
-  const WinTiles wt = win_tiles(g, a0, a0 + BT - 1, TS);
-  const int N = win_count(wt);
   auto slot_of = [&](int m) { return m % C::kSlots; };
   auto phase_of = [&](int m) { return (uint32_t)(m / C::kSlots) & 1; };
 
@@ -576,81 +678,64 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorM
       }
     }
   } else if (warp == kMmaWarp) {
-    const bool issuer = elect_one_sync();
-    const uint32_t sbase = smem_u32(smem);
-    auto all = [&](bool r) { return __all_sync(0xffffffffu, r) != 0; };
-    auto slot_addr = [&](int n) { return sbase + slot_of(n) * C::kSlotBytes; };
-    auto issue_sd = [&](int n) -> bool {
-      if (!all(mbar_wait(&full[slot_of(n)], phase_of(n), wd))) return false;
-      tc_fence_after();
-      const int b = n & 1;
-      const uint64_t bk = smem_desc_sw128(slot_addr(n), 0, 1024);
-      const uint64_t bv = smem_desc_sw128(slot_addr(n) + C::kStepTileBytes, 0, 1024);
+    if (elect_one_sync()) {
+      const uint32_t sbase = smem_u32(smem);
+      RingPos<C::kSlots> in, use;  // steps of the next S and of the next dQ
+      auto issue_sd = [&](int b) -> bool {
+        if (!mbar_wait(&full[in.slot], in.phase, wd)) return false;
+        tc_fence_after();
+        const uint32_t at = sbase + in.slot * C::kSlotBytes;
+        const uint64_t bk = smem_desc_sw128(at, 0, 1024);
+        const uint64_t bv = smem_desc_sw128(at + C::kStepTileBytes, 0, 1024);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)  // K step k: dims 16k..16k+15 = packed columns 8k..8k+7
-        if (issuer) mma_ts(tmem + col_s(b), tmem + kColQ + 8 * k, kmajor_step<kStepBoxBytes>(bk, k), kIdescSS, k > 0);
+        for (int k = 0; k < D / 16; ++k)  // K step k: dims 16k..16k+15 = packed columns 8k..8k+7
+          mma_ts(tmem + col_s(b), tmem + kColQ + 8 * k, kmajor_step<kStepBoxBytes>(bk, k), kIdescSS, k > 0);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        if (issuer) mma_ts(tmem + col_dp(b), tmem + kColDO + 8 * k, kmajor_step<kStepBoxBytes>(bv, k), kIdescSS, k > 0);
-      if (issuer) mma_commit(&bars[kB_SFull + b]);
-      return true;
-    };
-    bool ok = N > 0 && all(mbar_wait(&bars[kB_QReady], 0, wd));
-    if (ok) {
-      tc_fence_after();
-      ok = issue_sd(0);
-    }
-    if (ok && N > 1) ok = issue_sd(1);
-    for (int n = 0; ok && n < N; ++n) {
-      const int b = n & 1;
-      if (!(ok = all(mbar_wait(&bars[kB_PReady + b], (uint32_t)((n >> 1) & 1), wd)))) break;
-      tc_fence_after();
-      const uint64_t mk = smem_desc_sw128(slot_addr(n), kStepBoxBytes, 1024);
+        for (int k = 0; k < D / 16; ++k)
+          mma_ts(tmem + col_dp(b), tmem + kColDO + 8 * k, kmajor_step<kStepBoxBytes>(bv, k), kIdescSS, k > 0);
+        mma_commit(&bars[kB_SFull + b]);
+        in.next();
+        return true;
+      };
+      bool ok = N > 0 && mbar_wait(&bars[kB_QReady], 0, wd);
+      if (ok) {
+        tc_fence_after();
+        ok = issue_sd(0);
+      }
+      if (ok && N > 1) ok = issue_sd(1);
+      for (int n = 0; ok && n < N; ++n, use.next()) {
+        const int b = n & 1;
+        const uint64_t mk = smem_desc_sw128(sbase + use.slot * C::kSlotBytes, kStepBoxBytes, 1024);
+        if (!(ok = mbar_wait(&bars[kB_PReady + b], (uint32_t)((n >> 1) & 1), wd))) break;
+        tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < TS / 16; ++k)  // dQ += dS K, both terms of dS
-        if (issuer) {
+        for (int k = 0; k < TS / 16; ++k) {  // dQ += dS K, both terms of dS
           mma_ts(tmem + kColAcc, tmem + col_s(b) + packed_step_col(k), mnmajor_step(mk, k), C::kIdescTS,
                  !(n == 0 && k == 0));
           mma_ts(tmem + kColAcc, tmem + col_dp(b) + packed_step_col(k), mnmajor_step(mk, k), C::kIdescTS, 1);
         }
-      if (issuer) mma_commit(&empty[slot_of(n)]);
-      if (n + 2 < N && !(ok = issue_sd(n + 2))) break;
-    }
-    if (issuer) {
+        mma_commit(&empty[use.slot]);
+        if (n + 2 < N && !(ok = issue_sd(b))) break;
+      }
       mma_commit(&bars[kB_Done]);
       mma_commit(&bars[kB_Drain]);
+      drain_wait(&bars[kB_Drain], 0, p.watchdog_ns);
     }
-    drain_wait(&bars[kB_Drain], 0, p.watchdog_ns);
+    __syncwarp();
   } else if (warp < kEwWarps) {
     // warp = 4 hh + wq: TMEM lanes 32 wq (query rows), keys 32 hh .. 32 hh + 31 of a step
     const int wq = warp % 4, hh = warp / 4;
     const int64_t a = a0 + wq * 32 + lane;
-    const int64_t stat = (int64_t)bh_q * p.s_pad + a;  // a < s_pad always
-    const float row_lse2 = p.lse2[stat];
-    const float row_delta = p.delta[stat];
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const bool row_ok = a < g.S;
     {
-      // this thread's row, dims (D/2) hh .., as bf16 pairs (the memory order); rows past the
-      // sequence are zeros
-      const int64_t base = ((int64_t)bh_q * g.S + (row_ok ? a : 0)) * D + (D / 2) * hh;
-      uint32_t x[D / 4];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const uint16_t* src = (t == 0 ? p.q : p.dout) + base;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint4 v4 = row_ok ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-          x[4 * c] = v4.x;
-          x[4 * c + 1] = v4.y;
-          x[4 * c + 2] = v4.z;
-          x[4 * c + 3] = v4.w;
-        }
         const uint32_t dst = tmem + lane_off + (t == 0 ? kColQ : kColDO) + (D / 4) * hh;
         if constexpr (D == 128)
-          tmem_st32(dst, x);
+          tmem_st32(dst, rows[t]);
         else
-          tmem_st16(dst, x);
+          tmem_st16(dst, rows[t]);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -662,16 +747,18 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorM
       const int b = n & 1;
       if (!(ok = mbar_wait(&bars[kB_SFull + b], (uint32_t)((n >> 1) & 1), wd))) break;
       tc_fence_after();
-      const WinCut cut = win_cut(g, a, (int64_t)win_tile(wt, n) * TS, TS);
-      const uint32_t see = range_bits(cut.lo, cut.hi, 32 * hh) | range_bits(0, min(cut.sk, cut.hi), 32 * hh);
-      uint32_t sv[32], dpv[32], pp[16], pds[16];
+      const uint32_t see = query_sees(g, a0, a, (int64_t)win_tile(wt, n) * TS, 32 * hh);
+      uint32_t sv[32], dpv[32], pds[16], rest[16];
       tmem_ld32(tmem + lane_off + col_s(b) + 32 * hh, sv);
       tmem_ld32(tmem + lane_off + col_dp(b) + 32 * hh, dpv);
       tmem_wait_ld();
       // only dS feeds the dQ product: its rounding to bf16 and the rounding of the rest
-      p_ds_chunk<false>(sv, dpv, nullptr, nullptr, row_lse2, row_delta, p.scale_log2, see, pp, pds);
+      if (see == 0xffffffffu)
+        ds_query<true>(sv, dpv, row_nlse2, row_ndelta, p.scale_log2, see, pds, rest);
+      else
+        ds_query<false>(sv, dpv, row_nlse2, row_ndelta, p.scale_log2, see, pds, rest);
       tmem_st16(tmem + lane_off + col_s(b) + 32 * hh, pds);
-      tmem_st16(tmem + lane_off + col_dp(b) + 32 * hh, pp);
+      tmem_st16(tmem + lane_off + col_dp(b) + 32 * hh, rest);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -749,8 +836,8 @@ int launch(const void* q, const void* k, const void* v, const void* out, const f
   p.plan = make_plan(g);
   p.q = static_cast<const uint16_t*>(q);
   p.dout = static_cast<const uint16_t*>(dout);
-  p.lse2 = scratch;
-  p.delta = scratch + rows;
+  p.nlse2 = scratch;
+  p.ndelta = scratch + rows;
   p.s_pad = (g.S + BT - 1) / BT * BT;
   p.parts = scratch + 2 * rows;
   p.scale = scale;
@@ -811,9 +898,10 @@ int64_t window_bwd_visits(const WinGeom& g, int pass, int32_t* counts) {
       for (int h = U.h0; h < U.h1; ++h)
         for (int64_t s = U.s0; s < U.s1; ++s, ++visits)
           for (int64_t u = U.kt * BT; u < (U.kt + 1) * BT; ++u) {
-            const int64_t past = u < g.sinks || u + g.window > g.S ? g.S : u + g.window;
+            int64_t in0, in1;
+            inner_steps(g, U.kt, in0, in1);
             for (int hh = 0; hh < 2; ++hh) {
-              const uint32_t see = range_bits(win_clip(u - s * TS, TS), win_clip(past - s * TS, TS), 32 * hh);
+              const uint32_t see = key_sees(u, key_past(g, u), s, 32 * hh, in0, in1);
               for (int e = 0; e < 32; ++e)
                 if (see >> e & 1) {
                   const int64_t t = s * TS + 32 * hh + e;
@@ -829,10 +917,8 @@ int64_t window_bwd_visits(const WinGeom& g, int pass, int32_t* counts) {
     const WinTiles wt = win_tiles(g, a0, a0 + BT - 1, TS);
     for (int n = 0; n < win_count(wt); ++n, ++visits)
       for (int64_t a = a0; a < a0 + BT && a < g.S; ++a) {
-        const WinCut cut = win_cut(g, a, (int64_t)win_tile(wt, n) * TS, TS);
         for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t see =
-              range_bits(cut.lo, cut.hi, 32 * hh) | range_bits(0, cut.sk < cut.hi ? cut.sk : cut.hi, 32 * hh);
+          const uint32_t see = query_sees(g, a0, a, (int64_t)win_tile(wt, n) * TS, 32 * hh);
           for (int e = 0; e < 32; ++e)
             if (see >> e & 1) counts[a * g.S + (int64_t)win_tile(wt, n) * TS + 32 * hh + e] += 1;
         }
