@@ -1,12 +1,12 @@
 // Causal attention with a sliding window and sinks, forward, for sm_100a (bf16; D = 128 on
-// CTA pairs, D = 64 on single CTAs).
+// CTA pairs, D = 64 and small problems on single CTAs).
 //
 // Mathematics: the blockwise online softmax of the ring kernels (softmax_rows.cuh) over the
 // keys that win_tiles lists; lse = m + ln l. Exponentials come from the special-function
 // unit alone, so lse is good to a few units in its last place.
 //
 // What bounds it: the tensor cores (4 D flops per visible pair; 128 of 4096 keys a row sees
-// cost a byte each from L2). A unit is two query tiles of 128 * CTAS rows: in a pair one
+// cost a byte each from L2). A unit is one or two query tiles of 128 * CTAS rows: in a pair one
 // M = 256 product covers a tile of both CTAs and each CTA stages half of every K and V
 // tile, which is what lets shared memory feed the products. Each query tile walks only the
 // key tiles that its own rows see: of a unit's two tiles the first skips the key tiles past
@@ -27,7 +27,6 @@ namespace winfwd {
 
 constexpr int BM = 128;   // query rows of a tile in one CTA (TMEM lanes)
 constexpr int BN = 128;   // keys per tile
-constexpr int NQ = 2;     // query tiles per unit
 constexpr int BOXW = 64;
 constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168;
@@ -42,7 +41,7 @@ constexpr float kSpecMaxSum = 1048576.0f;   // 2^20, see the softmax
 constexpr int kSmemLimit = 232448;
 constexpr uint32_t kTmemCols = 512;
 
-template <int D, int CTAS>
+template <int D, int CTAS, int NQ>  // NQ: query tiles per unit, 1 or 2
 struct Cfg {
   static constexpr int kQTileBytes = BM * D * 2;
   static constexpr int kQBoxBytes = BM * BOXW * 2;
@@ -87,11 +86,11 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
   }
 }
 
-template <int D, int CTAS>
+template <int D, int CTAS, int NQ>
 __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Params p) {
-  using C = Cfg<D, CTAS>;
+  using C = Cfg<D, CTAS, NQ>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -152,7 +151,9 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
   constexpr int kRowsQ = CTAS * BM;
   const WinTiles all = win_tiles(g, a0, a0 + C::kUnitRows - 1, BN);
   const int N = win_count(all);
-  const WinTiles tq[NQ] = {win_tiles(g, a0, a0 + kRowsQ - 1, BN), win_tiles(g, a0 + kRowsQ, a0 + 2 * kRowsQ - 1, BN)};
+  WinTiles tq[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) tq[q] = win_tiles(g, a0 + q * kRowsQ, a0 + (q + 1) * kRowsQ - 1, BN);
 
   if (warp >= 8) {
     regs_decrease<kRegsOther>();
@@ -251,8 +252,12 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
       auto kphase = [&](int n) { return (uint32_t)((2 * n) / C::kSlots) & 1; };
       auto vslot = [&](int n) { return (2 * n + 1) % C::kSlots; };
       auto vphase = [&](int n) { return (uint32_t)((2 * n + 1) / C::kSlots) & 1; };
-      int done[NQ] = {0, 0};                                       // key tiles of query tile q finished
-      const int total[NQ] = {win_count(tq[0]), win_count(tq[1])};
+      int done[NQ], total[NQ];  // key tiles of query tile q: finished, all
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        done[q] = 0;
+        total[q] = win_count(tq[q]);
+      }
       bool ok = N > 0 && wait_all(&bars[kQFull], 0);
       if (ok) ok = wait_all(&full[kslot(0)], kphase(0));
       if (ok) {
@@ -309,8 +314,8 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_off + C::kColO + q * D;
     const uint32_t leader_p = CTAS == 2 ? mapa_shared(smem_u32(&bars[kPReady + q]), 0) : 0;
     const float NEG_INF = -INFINITY;
-    const WinTiles mine = q == 0 ? tq[0] : tq[1];
-    const int n_mine = win_count(mine);
+    const WinTiles mine = q == 0 ? tq[0] : tq[NQ - 1];
+    const int n_mine = q < NQ ? win_count(mine) : 0;
     float m_ref = NEG_INF;
     float l = 0.f;
     bool ok = true;
@@ -342,13 +347,14 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
         // and moves the reference where that exceeds it by more than kRescaleLog2.
         load_scores();
         float lb = 0.f;
-        bool fast = __all_sync(0xffffffffu, m_ref != NEG_INF);
+        const bool started = __all_sync(0xffffffffu, m_ref != NEG_INF);
+        bool fast = started;
         if (fast) {
           lb = exp_pack_phased<BN, 0>(sr, p.scale_log2, m_ref, pk);
           fast = __all_sync(0xffffffffu, lb <= kSpecMaxSum);
         }
         if (!fast) {
-          load_scores();
+          if (started) load_scores();  // the exponentials took their place
           const float mblk = raw_rowmax<BN>(sr) * p.scale_log2;
           float alpha = 1.f;
           bool resc = false;
@@ -399,10 +405,10 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, int CTAS>
+template <int D, int CTAS, int NQ>
 int launch(const void* q, const void* k, const void* v, void* out, float* lse, const WinGeom& g, float scale,
            int* status, uint64_t watchdog_ns, cudaStream_t stream) {
-  using C = Cfg<D, CTAS>;
+  using C = Cfg<D, CTAS, NQ>;
   CUtensorMap mq, mk, mv;
   int rc;
   if ((rc = encode_rows_map(&mq, q, (int64_t)g.B * g.Hq, g.S, D, BM)) != 0) return rc;
@@ -416,7 +422,7 @@ int launch(const void* q, const void* k, const void* v, void* out, float* lse, c
   p.scale_log2 = scale * 1.4426950408889634f;
   p.blocks = (g.S + C::kUnitRows - 1) / C::kUnitRows;
   p.watchdog_ns = watchdog_ns;
-  auto kern = window_fwd_kernel<D, CTAS>;
+  auto kern = window_fwd_kernel<D, CTAS, NQ>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
     return RING_ATTN_ECUDA;
   cudaFuncAttributes fa;
@@ -428,22 +434,40 @@ int launch(const void* q, const void* k, const void* v, void* out, float* lse, c
   return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
 }
 
+// CTAs of a unit and its query tiles. Where one CTA per query tile of 128 rows still runs in
+// one wave, that is the shorter chain: a tile's softmax has the special-function unit to
+// itself (window 256, 4 heads, us, alone / in units: D = 64, S 1024 12.7 / 17.5 and 4096 14.8 /
+// 19.4; D = 128 14.5 / 26.7 and 15.0 / 27.2). Past one wave the units' shared key tiles win
+// (D = 64, S 8192: 24.5 / 19.4; D = 128, window 2048, S 8192: 75.8 / 54.4).
+struct Shape {
+  int ctas, nq;
+};
+Shape shape_of(const WinGeom& g) {
+  if ((int64_t)g.B * g.Hq * ((g.S + BM - 1) / BM) <= 148) return {1, 1};
+  return {g.D == 64 ? 1 : 2, 2};
+}
+
 }  // namespace winfwd
 
 int launch_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse, const WinGeom& g,
                       float scale, int* status, uint64_t watchdog_ns, cudaStream_t stream) {
-  if (g.D == 64) return winfwd::launch<64, 1>(q, k, v, out, lse, g, scale, status, watchdog_ns, stream);
-  return winfwd::launch<128, 2>(q, k, v, out, lse, g, scale, status, watchdog_ns, stream);
+  const winfwd::Shape x = winfwd::shape_of(g);
+  if (g.D == 64)
+    return x.nq == 1 ? winfwd::launch<64, 1, 1>(q, k, v, out, lse, g, scale, status, watchdog_ns, stream)
+                     : winfwd::launch<64, 1, 2>(q, k, v, out, lse, g, scale, status, watchdog_ns, stream);
+  return x.nq == 1 ? winfwd::launch<128, 1, 1>(q, k, v, out, lse, g, scale, status, watchdog_ns, stream)
+                   : winfwd::launch<128, 2, 2>(q, k, v, out, lse, g, scale, status, watchdog_ns, stream);
 }
 
 // The forward kernel's walk on the host: per unit the union of tiles in order, each query
 // tile taking those that win_has lists for it, the per-element cut as the softmax applies it.
 int64_t window_fwd_visits(const WinGeom& g, int32_t* counts) {
-  const int rows_q = g.D == 64 ? 128 : 256;
+  const winfwd::Shape x = winfwd::shape_of(g);
+  const int rows_q = x.ctas * winfwd::BM;
   int64_t visits = 0;
-  for (int64_t a0 = 0; a0 < g.S; a0 += 2 * rows_q) {
-    const WinTiles all = win_tiles(g, a0, a0 + 2 * rows_q - 1, winfwd::BN);
-    for (int q = 0; q < winfwd::NQ; ++q) {
+  for (int64_t a0 = 0; a0 < g.S; a0 += x.nq * rows_q) {
+    const WinTiles all = win_tiles(g, a0, a0 + x.nq * rows_q - 1, winfwd::BN);
+    for (int q = 0; q < x.nq; ++q) {
       const WinTiles t = win_tiles(g, a0 + q * rows_q, a0 + (q + 1) * rows_q - 1, winfwd::BN);
       int n = 0;
       for (int i = 0; i < win_count(all); ++i) {
@@ -454,9 +478,9 @@ int64_t window_fwd_visits(const WinGeom& g, int32_t* counts) {
         ++visits;
         for (int64_t a = a0 + q * rows_q; a < a0 + (q + 1) * rows_q && a < g.S; ++a) {
           const WinCut c = win_cut(g, a, (int64_t)tile * winfwd::BN, winfwd::BN);
-          for (int x = 0; x < c.hi; ++x)
-            if (win_whole(c, winfwd::BN) || (!win_none(c) && (x >= c.lo || x < c.sk)))
-              counts[a * g.S + (int64_t)tile * winfwd::BN + x] += 1;
+          for (int e = 0; e < c.hi; ++e)
+            if (win_whole(c, winfwd::BN) || (!win_none(c) && (e >= c.lo || e < c.sk)))
+              counts[a * g.S + (int64_t)tile * winfwd::BN + e] += 1;
         }
       }
       if (n != win_count(t)) return -1;

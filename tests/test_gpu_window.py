@@ -77,6 +77,21 @@ def test_forward_and_gradients(cuda_lib, D, shape):
     backward(q, k, v, do, out, lse, ref[3], W, sinks, str(shape))
 
 
+# more query tiles than SMs: the forward's units of two tiles, the backward without divided heads
+MANY = [(40, 2, 2, 129, 64, 3), (26, 2, 2, 300, 1, 0), (8, 4, 1, 513, 100, 5), (10, 3, 3, 640, 128, 128),
+        (3, 6, 2, 1025, 257, 130)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "-".join(map(str, s)))
+def test_many_tiles(cuda_lib, D, shape):
+    B, Hq, Hkv, S, W, sinks = shape
+    assert B * Hq * ((S + 127) // 128) > 148
+    q, k, v, do = inputs(B, Hq, Hkv, S, D, 17)
+    out, lse, ref = forward(q, k, v, W, sinks, str(shape))
+    backward(q, k, v, do, out, lse, ref[3], W, sinks, str(shape))
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_rows_of_a_long_sequence(cuda_lib, D):
     """Rows and keys picked from a long sequence (units in the middle, the cut sink tiles and their parts)."""

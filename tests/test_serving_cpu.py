@@ -104,7 +104,7 @@ WINDOWS = [(1, 1, 0), (5, 1, 0), (130, 64, 0), (300, 1, 3), (700, 100, 0), (700,
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("S,W,sinks", WINDOWS)
 def test_every_visible_pair_is_visited_once(lib, D, S, W, sinks):
-    for Hq, Hkv in ((1, 1), (6, 2)):
+    for Hq, Hkv in ((1, 1), (6, 2), (150, 150)):  # (one CTA per query tile, and in units)
         for pass_, times in ((0, 1), (1, Hq // Hkv), (2, 1)):
             counts = np.zeros((S, S), dtype=np.int32)
             n = B.ring_attn_debug_window_visit_counts(Hq, Hkv, S, D, W, sinks, pass_, counts.ctypes.data)
@@ -116,7 +116,8 @@ def test_window_visits_are_few(lib):
     """The walks stay near the visible pairs: no more than the tiles that the diagonal and the window cut."""
     S, W = 4096, 1024
     counts = np.zeros((S, S), dtype=np.int32)
-    assert B.ring_attn_debug_window_visit_counts(1, 1, S, 128, W, 4, 0, counts.ctypes.data) <= (S // 256) * (W // 128 + 3)
+    assert B.ring_attn_debug_window_visit_counts(8, 8, S, 128, W, 4, 0, counts.ctypes.data) <= (S // 256) * (W // 128 + 3)
+    assert B.ring_attn_debug_window_visit_counts(1, 1, S, 128, W, 4, 0, counts.ctypes.data) <= (S // 128) * (W // 128 + 2)
     assert B.ring_attn_debug_window_visit_counts(1, 1, S, 128, W, 0, 2, counts.ctypes.data) <= (S // 128) * (W // 64 + 2)
 
 
