@@ -561,7 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
 #pragma unroll 1
       for (int t = 0; it.next(p); ++t) {
         const int slot = t % C::kRaw;
-        if (!(wait_bar(&bars[kRawSeen + kv * kMaxRaw + slot], (uint32_t)(t / C::kRaw & 1), wd))) break;
+        // (both: V's form is also what the softmax of this tile packs to, and it starts after K)
+        if (!(wait_bar(&bars[kRawSeen + slot], (uint32_t)(t / C::kRaw & 1), wd))) break;
+        if (!(wait_bar(&bars[kRawSeen + kMaxRaw + slot], (uint32_t)(t / C::kRaw & 1), wd))) break;
         // the bulk copies' own barrier: their bytes are visible to those who wait on it
         if (!(wait_bar(&bars[kRawFull + slot], (uint32_t)(t / C::kRaw & 1), wd))) break;
         if (!(wait_bar(&free[t & 1], (uint32_t)(t >> 1 & 1) ^ 1, wd))) break;
