@@ -527,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
 
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = RING_ATTN_OK;  // the merge kernel reports
+  grid_let_next();
   if (warp == 0) warp_begin_walk(p, &s_walk);
   __syncthreads();
   Walk walk = s_walk;
@@ -835,24 +836,25 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   __shared__ float s_max[4];
   __shared__ float s_sum[kPar];
   __shared__ float4 s_acc[kPar][kTpr];
-  if (blockIdx.x == 0) report_bad(p);
   const int unit = blockIdx.x / p.rows_per_group;
   const int r = blockIdx.x - unit * p.rows_per_group;
   const int head = unit / p.groups, b = head / p.c.Hkv, kvh = head - b * p.c.Hkv;
   const int row = (unit - head * p.groups) * p.rows_per_group + r;
-  if (row >= p.T * p.rep) return;
   const Keys ks = sequence_keys(p, b);
-  const int64_t orow = out_row(p, b, kvh, row);
   const uint32_t per = unit_quads(p, ks);
   const int d4 = threadIdx.x % kTpr, part = threadIdx.x / kTpr;
+  if (per != 0 && threadIdx.x < 32) {
+    const Parts x = warp_parts(p, b, unit - b * p.c.Hkv * p.groups, per);
+    if (threadIdx.x == 0) s_parts = x;
+  }
+  grid_wait();
+  if (blockIdx.x == 0) report_bad(p);
+  if (row >= p.T * p.rep) return;
+  const int64_t orow = out_row(p, b, kvh, row);
   if (row >= ks.cnt * p.rep || per == 0) {
     if (threadIdx.x < D / 8) reinterpret_cast<uint4*>(p.out + orow * D)[threadIdx.x] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) p.lse[orow] = -INFINITY;
     return;
-  }
-  if (threadIdx.x < 32) {
-    const Parts x = warp_parts(p, b, unit - b * p.c.Hkv * p.groups, per);
-    if (threadIdx.x == 0) s_parts = x;
   }
   __syncthreads();
   const int parts = (int)s_parts.count;
@@ -903,69 +905,84 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   if (d4 == 0) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(tot)) * 0.69314718055994530942f;
 }
 
-// The same for units of many rows, whose parts are few: one warp per row.
-template <int D>
+// The same for units of many rows, whose parts are fewer. The unit's parts are found once for
+// 16 / G rows; G groups of 8 lanes share a row's parts: 4 where the rows alone leave SMs idle,
+// else 1 (12 units of 128 rows, D = 128, 13 parts: 4 groups 7 us, 1 group 13, a warp per row 10; 128 units, D = 64,
+// 2 parts: a warp per row 13 us, 1 group 6.5).
+template <int D, int G>
 __global__ void __launch_bounds__(128) tree_merge_rows_kernel(const __grid_constant__ Params p) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (blockIdx.x == 0) report_bad(p);
-  const int per_unit = p.rows_per_group / 4;
+  constexpr int kRows = 16 / G;  // per block
+  const int lane = threadIdx.x % 32, sub = lane % 8, grp = lane / 8 % G;
+  const int per_unit = p.rows_per_group / kRows;
   const int unit = blockIdx.x / per_unit;
-  const int r = (blockIdx.x - unit * per_unit) * 4 + warp;
+  const int r = (blockIdx.x - unit * per_unit) * kRows + threadIdx.x / (8 * G);
   const int head = unit / p.groups, b = head / p.c.Hkv, kvh = head - b * p.c.Hkv;
   const int row = (unit - head * p.groups) * p.rows_per_group + r;
-  if (row >= p.T * p.rep) return;
   const Keys ks = sequence_keys(p, b);
   const uint32_t per = unit_quads(p, ks);
+  Parts x{0u, 1u};
+  if (per != 0) x = warp_parts(p, b, unit - b * p.c.Hkv * p.groups, per);
+  grid_wait();
+  if (blockIdx.x == 0) report_bad(p);
+  if (row >= p.T * p.rep) return;
   const int64_t orow = out_row(p, b, kvh, row);
-  constexpr int kPer = D / 32;  // dimensions per lane
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer);
+  constexpr int kVec = D / 32;  // four neighbouring dimensions each, 32 apart
+  uint16_t* dst = p.out + orow * D + 4 * sub;
   if (row >= ks.cnt * p.rep || per == 0) {
 #pragma unroll
-    for (int e = 0; e < kPer / 2; ++e) dst[e] = 0u;
-    if (lane == 0) p.lse[orow] = -INFINITY;
+    for (int e = 0; e < kVec; ++e) *reinterpret_cast<uint2*>(dst + 32 * e) = make_uint2(0u, 0u);
+    if (sub + grp == 0) p.lse[orow] = -INFINITY;
     return;
   }
-  const Parts x = warp_parts(p, b, unit - b * p.c.Hkv * p.groups, per);
   const int parts = (int)x.count;
   if (parts == 1) return;
   const int64_t slot = (int64_t)x.first + unit;
   const float* lse = p.lse_parts + slot * p.rows_per_group + r;
-  const float* src = p.o_parts + (slot * p.rows_per_group + r) * D + lane * kPer;
+  const float* src = p.o_parts + (slot * p.rows_per_group + r) * D + 4 * sub;
+  const int64_t stride = (int64_t)p.rows_per_group * D;
+  const uint32_t row_lanes = G == 4 ? 0xffffffffu : 0xffu << (lane & 24);
   float M = -INFINITY;
 #pragma unroll 1
-  for (int i = lane; i < parts; i += 32) M = fmaxf(M, lse[(int64_t)i * p.rows_per_group]);
+  for (int i = sub + 8 * grp; i < parts; i += 8 * G) M = fmaxf(M, lse[(int64_t)i * p.rows_per_group]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float sum = 0.f, acc[kPer];
+  for (int o = 4 * G; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(row_lanes, M, o));
+  float sum = 0.f;
+  float4 acc[kVec];
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  for (int e = 0; e < kVec; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (M != -INFINITY) {
-    // lane i holds the weight of part i0 + i; the loads of the parts' rows do not wait for it
-#pragma unroll 1
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      const float mine = i0 + lane < parts ? ex2_approx(lse[(int64_t)(i0 + lane) * p.rows_per_group] - M) : 0.f;
-      const int n = min(32, parts - i0);
 #pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float w = __shfl_sync(0xffffffffu, mine, i);
-        const float* row_at = src + (int64_t)(i0 + i) * p.rows_per_group * D;
-        float v[kPer];
+    for (int i = grp; i < parts; i += G) {
+      const float w = ex2_approx(lse[(int64_t)i * p.rows_per_group] - M);
+      sum += w;
 #pragma unroll
-        for (int e = 0; e < kPer; e += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(row_at + e);
-          v[e] = x.x;
-          v[e + 1] = x.y;
-        }
-        sum += w;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, v[e], acc[e]);  // an empty part's row is 0 and so is w
+      for (int e = 0; e < kVec; ++e) {  // an empty part's row is 0 and so is its weight
+        const float4 v = *reinterpret_cast<const float4*>(src + i * stride + 32 * e);
+        acc[e].x = fmaf(w, v.x, acc[e].x);
+        acc[e].y = fmaf(w, v.y, acc[e].y);
+        acc[e].z = fmaf(w, v.z, acc[e].z);
+        acc[e].w = fmaf(w, v.w, acc[e].w);
       }
     }
   }
+#pragma unroll
+  for (int o = 8; o < 8 * G; o *= 2) {
+    sum += __shfl_xor_sync(row_lanes, sum, o);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      acc[e].x += __shfl_xor_sync(row_lanes, acc[e].x, o);
+      acc[e].y += __shfl_xor_sync(row_lanes, acc[e].y, o);
+      acc[e].z += __shfl_xor_sync(row_lanes, acc[e].z, o);
+      acc[e].w += __shfl_xor_sync(row_lanes, acc[e].w, o);
+    }
+  }
+  if (grp != 0) return;
   const float inv = M == -INFINITY ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int e = 0; e < kPer / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * 0.69314718055994530942f;
+  for (int e = 0; e < kVec; ++e)
+    *reinterpret_cast<uint2*>(dst + 32 * e) =
+        make_uint2(pack_bf16x2(acc[e].x * inv, acc[e].y * inv), pack_bf16x2(acc[e].z * inv, acc[e].w * inv));
+  if (sub == 0) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * 0.69314718055994530942f;
 }
 
 template <int FMT, int D, int NT>
@@ -986,6 +1003,10 @@ int launch_rows(const Params& p, cudaStream_t stream) {
 template <int FMT>
 int launch_rows_d(const Params& p, cudaStream_t stream) {
   return p.c.D == 64 ? launch_rows<FMT, 64>(p, stream) : launch_rows<FMT, 128>(p, stream);
+}
+
+int launch_merge(void (*kern)(Params), int64_t blocks, const Params& p, cudaStream_t stream) {
+  return launch_early(kern, (unsigned)blocks, 128, 0, stream, p) == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
 }
 
 inline int step_keys(int format, int D) { return format == RING_ATTN_CACHE_BF16 && D == 128 ? 16 : 32; }
@@ -1079,19 +1100,15 @@ int launch_tree(const CacheView& c, const void* q, const int64_t* qs, void* out,
   }
   if (rc) return rc;
   if (t.rows_per_group == 128) {
-    const unsigned blocks = (unsigned)(t.units * (t.rows_per_group / 4));
-    if (c.D == 64)
-      tree::tree_merge_rows_kernel<64><<<blocks, 128, 0, stream>>>(p);
-    else
-      tree::tree_merge_rows_kernel<128><<<blocks, 128, 0, stream>>>(p);
-  } else {
-    const unsigned blocks = (unsigned)(t.units * t.rows_per_group);
-    if (c.D == 64)
-      tree::tree_merge_kernel<64><<<blocks, 128, 0, stream>>>(p);
-    else
-      tree::tree_merge_kernel<128><<<blocks, 128, 0, stream>>>(p);
+    const int64_t rows = t.units * t.rows_per_group;
+    if (rows < 16 * 4 * 148)
+      return tree::launch_merge(c.D == 64 ? tree::tree_merge_rows_kernel<64, 4> : tree::tree_merge_rows_kernel<128, 4>,
+                                rows / 4, p, stream);
+    return tree::launch_merge(c.D == 64 ? tree::tree_merge_rows_kernel<64, 1> : tree::tree_merge_rows_kernel<128, 1>,
+                              rows / 16, p, stream);
   }
-  return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
+  return tree::launch_merge(c.D == 64 ? tree::tree_merge_kernel<64> : tree::tree_merge_kernel<128>,
+                            t.units * t.rows_per_group, p, stream);
 }
 
 }  // namespace ringattn

@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
 
   if (threadIdx.x == 0) {
     if (blockIdx.x == 0) *p.status = RING_ATTN_OK;
+    grid_let_next();
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars[kKFull + b], kFillWarps);
       mbar_init(&bars[kVFull + b], kFillWarps);

@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(256) window_prep_kernel(const uint16_t* __rest
                                                           float* __restrict__ ndelta, int64_t S, int64_t s_pad,
                                                           int64_t rows, int* status) {
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = RING_ATTN_OK;
+  grid_let_next();
   constexpr int kTpr = D / 8;
   const int64_t row = (int64_t)blockIdx.x * (256 / kTpr) + threadIdx.x / kTpr;
   const int sub = threadIdx.x % kTpr;
@@ -371,6 +372,7 @@ __device__ __forceinline__ void dkdv_unit(const CUtensorMap& tm_q, const CUtenso
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_wait();
   const Watchdog wd{abort_flag, p.status, p.watchdog_ns};
   const KeyUnit U = key_unit(g, p.plan, unit);
   const int rep = g.Hq / g.Hkv;
@@ -549,6 +551,7 @@ __device__ __forceinline__ void dkdv_unit(const CUtensorMap& tm_q, const CUtenso
 template <int D>
 __global__ void __launch_bounds__(256) window_reduce_kernel(const __grid_constant__ Params p, int64_t sink_items,
                                                             int64_t items) {
+  grid_wait();
   int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (it >= items) return;
   const Plan& pl = p.plan;
@@ -626,6 +629,7 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorM
         rows[t][4 * c + 3] = v4.w;
       }
     }
+    grid_wait();
     const int64_t stat = (int64_t)bh_q * p.s_pad + a;  // a < s_pad always
     row_nlse2 = p.nlse2[stat];
     row_ndelta = p.ndelta[stat];
@@ -788,6 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  grid_let_next();
   if (blockIdx.x < p.plan.units)
     dkdv_unit<D>(tm_q64, tm_do64, tm_k, tm_v, p, smem, blockIdx.x);
   else
@@ -866,15 +871,18 @@ int launch(const void* q, const void* k, const void* v, const void* out, const f
   p.dq = dq;
   p.dk = dk;
   p.dv = dv;
-  window_grads_kernel<D><<<(unsigned)(p.plan.units + q_units), kThreads, smem, stream>>>(mq, mdo, mk, mv, mk64, mv64, p);
-  if (cudaGetLastError() != cudaSuccess) return RING_ATTN_ECUDA;
+  if (launch_early(window_grads_kernel<D>, (unsigned)(p.plan.units + q_units), kThreads, smem, stream, mq, mdo, mk, mv,
+                   mk64, mv64, p) != cudaSuccess)
+    return RING_ATTN_ECUDA;
   const int64_t per_tile = bhk * 2 * BT * (D / 8);
   const int64_t sink_items = p.plan.segs * p.plan.splits > 1 ? per_tile * p.plan.sink_tiles : 0;
   const int64_t items = sink_items + (p.plan.splits > 1 ? per_tile * (p.plan.tiles - p.plan.sink_tiles) : 0);
   if (items == 0) return RING_ATTN_OK;
   if ((items + 255) / 256 > 0x7fffffff) return RING_ATTN_EINVAL;
-  window_reduce_kernel<D><<<(unsigned)((items + 255) / 256), 256, 0, stream>>>(p, sink_items, items);
-  return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
+  return launch_early(window_reduce_kernel<D>, (unsigned)((items + 255) / 256), 256, 0, stream, p, sink_items, items) ==
+                 cudaSuccess
+             ? RING_ATTN_OK
+             : RING_ATTN_ECUDA;
 }
 
 }  // namespace winbwd
