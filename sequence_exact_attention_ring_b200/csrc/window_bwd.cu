@@ -498,7 +498,7 @@ __device__ __forceinline__ void dkdv_unit(const CUtensorMap& tm_q, const CUtenso
           tmem_ld_frag16(tDP + (t << 20), dpv + 16 * t);
         }
         const bool whole = s >= in0 && s < in1;
-        if (!whole) {
+        if (__builtin_expect(!whole, 0)) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int64_t key = U.kt * BT + wq * 32 + 8 * x + fr;
@@ -506,7 +506,7 @@ __device__ __forceinline__ void dkdv_unit(const CUtensorMap& tm_q, const CUtenso
           }
         }
         tmem_wait_ld();
-        if (whole)
+        if (__builtin_expect(whole, 1))
           p_ds_keys<true>(sv, dpv, nlse2c, ndeltac, p.scale_log2, see, pp, pds);
         else
           p_ds_keys<false>(sv, dpv, nlse2c, ndeltac, p.scale_log2, see, pp, pds);
@@ -757,7 +757,7 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorM
       tmem_ld32(tmem + lane_off + col_dp(b) + 32 * hh, dpv);
       tmem_wait_ld();
       // only dS feeds the dQ product: its rounding to bf16 and the rounding of the rest
-      if (see == 0xffffffffu)
+      if (__builtin_expect(see == 0xffffffffu, 1))
         ds_query<true>(sv, dpv, row_nlse2, row_ndelta, p.scale_log2, see, pds, rest);
       else
         ds_query<false>(sv, dpv, row_nlse2, row_ndelta, p.scale_log2, see, pds, rest);

@@ -79,6 +79,16 @@ struct Params {
   uint64_t watchdog_ns;
 };
 
+// The 32 query rows from a_warp see the whole key tile at k0: most tiles, which need no mask.
+RA_HD bool warp_sees_all(const WinGeom& g, int64_t a_warp, int64_t k0) {
+  return k0 + BN - 1 <= a_warp && (k0 > a_warp + 31 - g.window || k0 + BN <= g.sinks);
+}
+RA_HD uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+// Columns c0 .. c0 + 31 that a row with this cut sees.
+RA_HD uint32_t cut_bits(const WinCut& cut, int c0) {
+  return low_bits(cut.hi - c0) & (~low_bits(cut.lo - c0) | low_bits(cut.sk - c0));
+}
+
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity)) {
@@ -202,104 +212,101 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kMmaWarp && leader) {
       // ---------------------------------------------------------------- MMA issuer
-      const uint32_t sbase = smem_u32(smem);
-      const uint64_t dq0 = smem_desc_sw128(sbase, 0, 1024);
-      const uint64_t dk0 = smem_desc_sw128(sbase + C::kOffKV, 0, 1024);
-      const uint64_t dv0 = smem_desc_sw128(sbase + C::kOffKV, C::kVBoxBytes, 1024);
-      const bool issuer = elect_one_sync();
-      auto issue_s = [&](int q, int slot) {
-        const uint64_t dq = dq0 + (uint64_t)((q * C::kQTileBytes) >> 4);
-        const uint64_t dk = dk0 + (uint64_t)((slot * C::kPartBytes) >> 4);
-        const uint32_t d = tmem + C::kColS + q * BN;
+      // (one thread: what passes between two products is time that the tensor pipe idles)
+      if (elect_one_sync()) {
+        const uint32_t sbase = smem_u32(smem);
+        const uint64_t dq0 = smem_desc_sw128(sbase, 0, 1024);
+        const uint64_t dk0 = smem_desc_sw128(sbase + C::kOffKV, 0, 1024);
+        const uint64_t dv0 = smem_desc_sw128(sbase + C::kOffKV, C::kVBoxBytes, 1024);
+        auto issue_s = [&](int q, int slot) {
+          const uint64_t dq = dq0 + (uint64_t)((q * C::kQTileBytes) >> 4);
+          const uint64_t dk = dk0 + (uint64_t)((slot * C::kPartBytes) >> 4);
+          const uint32_t d = tmem + C::kColS + q * BN;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t da = dq + (((k / 4) * C::kQBoxBytes + (k % 4) * 32) >> 4);
-          const uint64_t db = dk + (((k / 4) * C::kKBoxBytes + (k % 4) * 32) >> 4);
-          if (issuer) {
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t da = dq + (((k / 4) * C::kQBoxBytes + (k % 4) * 32) >> 4);
+            const uint64_t db = dk + (((k / 4) * C::kKBoxBytes + (k % 4) * 32) >> 4);
             if (CTAS == 2)
               mma_ss_2sm(d, da, db, C::kIdescQK, k > 0);
             else
               mma_ss(d, da, db, C::kIdescQK, k > 0);
           }
-        }
-      };
-      auto issue_pv = [&](int q, int slot, bool first) {
-        const uint64_t dv = dv0 + (uint64_t)((slot * C::kPartBytes) >> 4);
-        const uint32_t d = tmem + C::kColO + q * D;
-        const uint32_t pa = tmem + C::kColS + q * BN;
+        };
+        auto issue_pv = [&](int q, int slot, bool first) {
+          const uint64_t dv = dv0 + (uint64_t)((slot * C::kPartBytes) >> 4);
+          const uint32_t d = tmem + C::kColO + q * D;
+          const uint32_t pa = tmem + C::kColS + q * BN;
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k) {
-          if (issuer) {
+          for (int k = 0; k < BN / 16; ++k) {
             if (CTAS == 2)
               mma_ts_2sm(d, pa + k * 8, dv + ((k * 16 * 128) >> 4), C::kIdescPV, !(first && k == 0));
             else
               mma_ts(d, pa + k * 8, dv + ((k * 16 * 128) >> 4), C::kIdescPV, !(first && k == 0));
           }
-        }
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (issuer) {
+        };
+        auto commit = [&](uint64_t* bar) {
           if (CTAS == 2)
             mma_commit_2sm(bar, 0x3);
           else
             mma_commit(bar);
-        }
-      };
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, wd)) != 0;
-      };
-      auto kslot = [&](int n) { return (2 * n) % C::kSlots; };
-      auto kphase = [&](int n) { return (uint32_t)((2 * n) / C::kSlots) & 1; };
-      auto vslot = [&](int n) { return (2 * n + 1) % C::kSlots; };
-      auto vphase = [&](int n) { return (uint32_t)((2 * n + 1) / C::kSlots) & 1; };
-      int done[NQ], total[NQ];  // key tiles of query tile q: finished, all
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        done[q] = 0;
-        total[q] = win_count(tq[q]);
-      }
-      bool ok = N > 0 && wait_all(&bars[kQFull], 0);
-      if (ok) ok = wait_all(&full[kslot(0)], kphase(0));
-      if (ok) {
-        tc_fence_after();
-#pragma unroll
-        for (int q = 0; q < NQ; ++q)
-          if (win_has(tq[q], win_tile(all, 0))) {
-            issue_s(q, kslot(0));
-            commit(&bars[kSFull + q]);
-          }
-        commit(&empty[kslot(0)]);
-      }
-      // per key tile n: PV0(n), S0(n+1), PV1(n), S1(n+1), each only where the query tile meets
-      // the key tile. The commit that reports S_q covers the query tile's last PV.
-      for (int n = 0; ok && n < N; ++n) {
-        const int tile = win_tile(all, n);
-        const bool more = n + 1 < N;
-        const int next = more ? win_tile(all, n + 1) : 0;
-        if (!(ok = wait_all(&full[vslot(n)], vphase(n)))) break;
+        };
+        auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+          return mbar_wait_cluster(bar, parity, wd);
+        };
+        auto kslot = [&](int n) { return (2 * n) % C::kSlots; };
+        auto kphase = [&](int n) { return (uint32_t)((2 * n) / C::kSlots) & 1; };
+        auto vslot = [&](int n) { return (2 * n + 1) % C::kSlots; };
+        auto vphase = [&](int n) { return (uint32_t)((2 * n + 1) / C::kSlots) & 1; };
+        int done[NQ], total[NQ];  // key tiles of query tile q: finished, all
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
-          if (win_has(tq[q], tile)) {
-            if (!(ok = wait_all(&bars[kPReady + q], (uint32_t)(done[q] & 1)))) break;
-            tc_fence_after();
-            issue_pv(q, vslot(n), done[q] == 0);
-            if (++done[q] == total[q]) commit(&bars[kODone + q]);
-          }
-          if (more && q == 0) {
-            if (!(ok = wait_all(&full[kslot(n + 1)], kphase(n + 1)))) break;
-            tc_fence_after();
-          }
-          if (more && win_has(tq[q], next)) {
-            issue_s(q, kslot(n + 1));
-            commit(&bars[kSFull + q]);
-          }
+          done[q] = 0;
+          total[q] = win_count(tq[q]);
         }
-        if (!ok) break;
-        commit(&empty[vslot(n)]);
-        if (more) commit(&empty[kslot(n + 1)]);
+        bool ok = N > 0 && wait_all(&bars[kQFull], 0);
+        if (ok) ok = wait_all(&full[kslot(0)], kphase(0));
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < NQ; ++q)
+            if (win_has(tq[q], win_tile(all, 0))) {
+              issue_s(q, kslot(0));
+              commit(&bars[kSFull + q]);
+            }
+          commit(&empty[kslot(0)]);
+        }
+        // per key tile n: PV0(n), S0(n+1), PV1(n), S1(n+1), each only where the query tile meets
+        // the key tile. The commit that reports S_q covers the query tile's last PV.
+        for (int n = 0; ok && n < N; ++n) {
+          const int tile = win_tile(all, n);
+          const bool more = n + 1 < N;
+          const int next = more ? win_tile(all, n + 1) : 0;
+          if (!(ok = wait_all(&full[vslot(n)], vphase(n)))) break;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if (win_has(tq[q], tile)) {
+              if (!(ok = wait_all(&bars[kPReady + q], (uint32_t)(done[q] & 1)))) break;
+              tc_fence_after();
+              issue_pv(q, vslot(n), done[q] == 0);
+              if (++done[q] == total[q]) commit(&bars[kODone + q]);
+            }
+            if (more && q == 0) {
+              if (!(ok = wait_all(&full[kslot(n + 1)], kphase(n + 1)))) break;
+              tc_fence_after();
+            }
+            if (more && win_has(tq[q], next)) {
+              issue_s(q, kslot(n + 1));
+              commit(&bars[kSFull + q]);
+            }
+          }
+          if (!ok) break;
+          commit(&empty[vslot(n)]);
+          if (more) commit(&empty[kslot(n + 1)]);
+        }
+        commit(&bars[kDrain]);
+        drain_wait(&bars[kDrain], 0, p.watchdog_ns);
       }
-      commit(&bars[kDrain]);
-      drain_wait(&bars[kDrain], 0, p.watchdog_ns);
+      __syncwarp();
     } else if (warp == kMmaWarp && lane == 0) {
       drain_wait(&bars[kDrain], 0, p.watchdog_ns);
     }
@@ -308,7 +315,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------------- softmax (every CTA)
     const int q = warp / 4;
     const int wq = warp % 4;
-    const int64_t a = a0 + kRowsQ * q + BM * (int64_t)rank + wq * 32 + lane;
+    const int64_t a_warp = a0 + kRowsQ * q + BM * (int64_t)rank + wq * 32, a = a_warp + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::kColS + q * BN;
     const uint32_t tO = tmem + lane_off + C::kColO + q * D;
@@ -320,41 +327,40 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
     float l = 0.f;
     bool ok = true;
     for (int n = 0; n < n_mine; ++n) {
+      const int64_t k0 = (int64_t)win_tile(mine, n) * BN;
+      const bool whole = warp_sees_all(g, a_warp, k0);
       if (!(ok = mbar_wait_cluster(&bars[kSFull + q], (uint32_t)(n & 1), wd))) break;
       tc_fence_after();
-      const WinCut cut = win_cut(g, a, (int64_t)win_tile(mine, n) * BN, BN);
-      const bool whole = __all_sync(0xffffffffu, win_whole(cut, BN));
-      uint32_t sr[BN];
-      auto load_scores = [&]() {
+      if (__builtin_expect(!whole, 0)) {
+        // hidden scores are overwritten in place, by a loop: the straight path below stays short
+        const WinCut cut = win_cut(g, a, k0, BN);
+#pragma unroll 1
+        for (int c0 = 0; c0 < BN; c0 += 32) {
+          uint32_t x[32];
+          tmem_ld32(tS + c0, x);
+          const uint32_t see = cut_bits(cut, c0);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(see >> e & 1)) x[e] = 0xff800000u;  // -inf
+          tmem_st32(tS + c0, x);
+        }
+        tmem_wait_st();
+      }
+      // Exponentials against the current reference maximum first: O / l and lse do not
+      // depend on it, so a block whose row sums stay <= kSpecMaxSum (every P <= 2^20) is
+      // kept as is. Otherwise, and for a row's first block, the warp takes the block maximum
+      // and moves the reference where that exceeds it by more than kRescaleLog2.
+      uint32_t pk[BN / 2];
+      float lb;
+      bool fast = __all_sync(0xffffffffu, m_ref != NEG_INF);
+#pragma unroll 1
+      while (true) {
+        uint32_t sr[BN];
 #pragma unroll
         for (int c = 0; c < BN / 32; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
         tmem_wait_ld();
-        if (!whole) {
-#pragma unroll
-          for (int c = 0; c < BN; ++c)
-            sr[c] = (c < cut.hi && (c >= cut.lo || c < cut.sk)) ? sr[c] : 0xff800000u;  // -inf
-        }
-      };
-      uint32_t pk[BN / 2];
-      if (__all_sync(0xffffffffu, win_none(cut))) {
-        // no row of this warp sees the block: P = 0, state unchanged
-#pragma unroll
-        for (int c = 0; c < BN / 2; ++c) pk[c] = 0u;
-      } else {
-        // Exponentials against the current reference maximum first: O / l and lse do not
-        // depend on it, so a block whose row sums stay <= kSpecMaxSum (every P <= 2^20) is
-        // kept as is. Otherwise, and for a row's first block, the warp takes the block maximum
-        // and moves the reference where that exceeds it by more than kRescaleLog2.
-        load_scores();
-        float lb = 0.f;
-        const bool started = __all_sync(0xffffffffu, m_ref != NEG_INF);
-        bool fast = started;
-        if (fast) {
-          lb = exp_pack_phased<BN, 0>(sr, p.scale_log2, m_ref, pk);
-          fast = __all_sync(0xffffffffu, lb <= kSpecMaxSum);
-        }
         if (!fast) {
-          if (started) load_scores();  // the exponentials took their place
           const float mblk = raw_rowmax<BN>(sr) * p.scale_log2;
           float alpha = 1.f;
           bool resc = false;
@@ -367,10 +373,12 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads, 1)
           // S ready for this tile implies that this query tile's last PV completed: O is
           // stable (and not yet written before its first PV, which overwrites it)
           if (n > 0 && __any_sync(0xffffffffu, resc)) rescale_o<D>(tO, alpha);
-          lb = exp_pack_phased<BN, 0>(sr, p.scale_log2, (m_ref == NEG_INF) ? 0.f : m_ref, pk);
         }
-        l += lb;
+        lb = exp_pack_phased<BN, 0>(sr, p.scale_log2, (m_ref == NEG_INF) ? 0.f : m_ref, pk);
+        if (!fast || __all_sync(0xffffffffu, lb <= kSpecMaxSum)) break;
+        fast = false;
       }
+      l += lb;
 #pragma unroll
       for (int c = 0; c < BN / 64; ++c) tmem_st32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[c * 32]));
       tmem_wait_st();
@@ -460,7 +468,7 @@ int launch_window_fwd(const void* q, const void* k, const void* v, void* out, fl
 }
 
 // The forward kernel's walk on the host: per unit the union of tiles in order, each query
-// tile taking those that win_has lists for it, the per-element cut as the softmax applies it.
+// tile taking those that win_has lists for it, the masks as the softmax applies them.
 int64_t window_fwd_visits(const WinGeom& g, int32_t* counts) {
   const winfwd::Shape x = winfwd::shape_of(g);
   const int rows_q = x.ctas * winfwd::BM;
@@ -477,10 +485,14 @@ int64_t window_fwd_visits(const WinGeom& g, int32_t* counts) {
         ++n;
         ++visits;
         for (int64_t a = a0 + q * rows_q; a < a0 + (q + 1) * rows_q && a < g.S; ++a) {
-          const WinCut c = win_cut(g, a, (int64_t)tile * winfwd::BN, winfwd::BN);
-          for (int e = 0; e < c.hi; ++e)
-            if (win_whole(c, winfwd::BN) || (!win_none(c) && (e >= c.lo || e < c.sk)))
-              counts[a * g.S + (int64_t)tile * winfwd::BN + e] += 1;
+          const int64_t k0 = (int64_t)tile * winfwd::BN;
+          const bool whole = winfwd::warp_sees_all(g, a - (a - a0) % 32, k0);
+          const WinCut cut = win_cut(g, a, k0, winfwd::BN);
+          for (int c0 = 0; c0 < winfwd::BN; c0 += 32) {
+            const uint32_t see = whole ? 0xffffffffu : winfwd::cut_bits(cut, c0);
+            for (int e = 0; e < 32; ++e)
+              if (see >> e & 1) counts[a * g.S + k0 + c0 + e] += 1;
+          }
         }
       }
       if (n != win_count(t)) return -1;
