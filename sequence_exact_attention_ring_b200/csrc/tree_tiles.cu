@@ -673,30 +673,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
         const int t = t0 + n;
         if ((t & 1) != hh) continue;
         const int kb = step_key(p, ks, part.q0 + n);
-        if (!(ok = (wait_bar(&bars[kSFull + hh], (uint32_t)(t >> 1 & 1), wd)))) break;
-        tc_fence_after();
-        const uint32_t tS = tmem + lane_off + 128 * hh;
         // every row sees the whole tile
         const bool whole = kb + TK <= ks.n &&
                            (p.window <= 0 || kb + TK <= p.sinks || kb >= ks.n + p.T - p.window);
+        if (!(ok = (wait_bar(&bars[kSFull + hh], (uint32_t)(t >> 1 & 1), wd)))) break;
+        tc_fence_after();
+        const uint32_t tS = tmem + lane_off + 128 * hh;
+        if (__builtin_expect(!whole, 0)) {
+          // hidden scores are overwritten in place, by a loop: the straight path below stays
+          // short (what the roles share is the instruction caches)
+          const int hi = clip(ks.n - kb), lo = clip(lo_key - kb), sk = min(clip(p.sinks - kb), hi);
+#pragma unroll 1
+          for (int c0 = 0; c0 < TK; c0 += 32) {
+            uint32_t x[32];
+            tmem_ld32(tS + c0, x);
+            const int j0 = kb + c0 - ks.n;  // drafted node of the chunk's first column
+            const uint32_t drafts = j0 >= 64 || j0 <= -32 ? 0u : (uint32_t)(j0 >= 0 ? seen >> j0 : seen << -j0);
+            const uint32_t see = span_bits(lo, hi, c0) | span_bits(0, sk, c0) | drafts;
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see >> e & 1)) x[e] = 0xff800000u;  // -inf
+            tmem_st32(tS + c0, x);
+          }
+          tmem_wait_st();
+        }
         uint32_t sr[64];
-        const int hi = clip(ks.n - kb), lo = clip(lo_key - kb), sk = min(clip(p.sinks - kb), hi);
         auto load = [&](int c0) {  // columns c0 .. c0 + 63
           tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
           tmem_ld32(tS + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
           tmem_wait_ld();
-          if (__builtin_expect(!whole, 0)) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int c1 = c0 + 32 * c;
-              const int j0 = kb + c1 - ks.n;  // drafted node of the chunk's first column
-              const uint32_t drafts = j0 >= 64 || j0 <= -32 ? 0u : (uint32_t)(j0 >= 0 ? seen >> j0 : seen << -j0);
-              const uint32_t see = span_bits(lo, hi, c1) | span_bits(0, sk, c1) | drafts;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(see >> e & 1)) sr[32 * c + e] = 0xff800000u;  // -inf
-            }
-          }
         };
         float top = -INFINITY;
 #pragma unroll 1  // (one copy of the code each: the roles share the instruction caches)
