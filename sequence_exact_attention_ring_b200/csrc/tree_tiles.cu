@@ -5,23 +5,28 @@
 // product: S = Q K^T with Q in tensor memory, O += P V with P in tensor memory, 128 cache
 // rows at a time.
 //
-// What bounds it: the tensor cores (4 * 128 * 128 * D flops per tile of 128 rows, whatever
-// part of the group's rows is real), the exponentials (128 x 128 per tile at 16 a clock: as
-// long as the products at D = 128) and, with codes, their conversion. The cache's rows are
-// contiguous and come in as they are, by bulk copies into a ring of raw tiles; eight warps
-// convert them, 8 elements at a time, into the swizzled K and V tiles that the products read.
-// bf16 rows are copied straight into those tiles.
+// Floors: the tensor cores (4 * 128 * 128 * D flops per tile of 128 rows, whatever part of
+// the group's rows is real), the exponentials (128 x 128 per tile at 16 a clock: as long as
+// the products at D = 128) and, with codes, their conversion. What bounds it as built is the
+// chain of one softmax warp (scores ready, maxima, reference, exponentials, P), 4400 clocks a
+// tile, of which two run at a time: 148 CTAs take 60 us for 12 groups of 116 rows and 50k keys
+// of e2m1 (D = 128, 17 us of products), 100 us for 128 full groups and 8k keys of e4m3 (D = 64,
+// 21 us). The cache's rows are contiguous and come in as they are, by bulk copies into a ring of
+// raw tiles; eight warps convert them, 8 elements at a time, into the swizzled K and V tiles
+// that the products read. bf16 rows are copied straight into those tiles.
 //
 // Roles (640 threads): warps 0-3 softmax of the even tiles, warps 4-7 of the odd ones (warp w:
 // rows 32 (w % 4) ..), warps 8-11 fill K tiles, warps 12-15 V tiles, warp 16 issues the
-// products, warp 17 fetches raw tiles, warps 18 and 19 look at their scales. A softmax warp first takes
-// its tile's row maxima and hands the row's reference maximum to the warp of the next tile,
-// then exponentiates while that one is already at its maxima: the chain from tile to tile is
-// the short first half only. (With both warps on one tile, 64 columns each, a tile took 5000
-// clocks: every step of the chain waited for the one before.) Tensor memory: S double-buffered
-// [0,128) and [128,256), O [256,384), Q [384,448) and, in bf16, [448,512). Every role walks
-// the CTA's share of the work by itself (tree_common.cuh), so tiles of the next unit are
-// filled while the last one is finished.
+// products, warp 17 fetches raw tiles, warps 18 and 19 look at their scales. A softmax warp first
+// takes its tile's row maxima and hands the row's reference maximum to the warp of the next
+// tile, then exponentiates while that one is already at its maxima: the chain from tile to
+// tile is the short first half only. (Both warps on one tile, 64 columns each: 5000 clocks a
+// tile, as every step of the chain waited for the one before. Sixteen softmax warps of 64
+// columns, or the reference taken on trust and checked by the sums: within 3 % of this.)
+// Tensor memory: S of three tiles at D = 64, of two at D = 128, then O, Q and its bf16 form;
+// with the third the scores of a set's next tile are there when it ends one (D = 64: 119 ->
+// 107 us). Every role walks the CTA's share of the work by itself (tree_common.cuh), so tiles
+// of the next unit are filled while the last one is finished.
 //
 // Codes become fp16 operands as in tree_rows.cu, two per conversion instruction, times their
 // block's scale and 2^6 (e4m3) or 2^8 (e2m1): fp16 then holds every value of a block exactly
@@ -63,18 +68,22 @@ constexpr int kRegsSoftmax = 144, kRegsFill = 72, kRegsOther = 48;
 static_assert(2 * kRegsSoftmax + 2 * kRegsFill + kRegsOther <= 5 * kLaunchRegs, "register split exceeds the launch pool");
 constexpr int kBoxBytes = TK * 128;  // 128 rows x 64 elements
 constexpr int kSmemLimit = 232448;
-constexpr uint32_t kTmemCols = 512, kColO = 256, kColQ = 384, kColQb = 448;
+constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxRaw = 4;
 constexpr int kFlags = 16;  // tiles whose form is remembered (more than are ever in flight)
 
-enum Bar { kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kSFull = 8, kPReady = 10, kPvDone = 12, kQReady = 13,
-           kODone = 14, kDrain = 15, kPair = 16, kMax = 20, kRawFull = 28, kRawFree = kRawFull + kMaxRaw,
+enum Bar { kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kPReady = 8, kPvDone = 10, kQReady = 11, kODone = 12,
+           kDrain = 13, kPair = 14, kMax = 18, kSFull = 26, kRawFull = 29, kRawFree = kRawFull + kMaxRaw,
            kRawSeen = kRawFree + kMaxRaw, kNumBars = kRawSeen + 2 * kMaxRaw };
 
 template <int FMT, int D>
 struct Cfg {
   static constexpr bool kMx = FMT != RING_ATTN_CACHE_BF16;
   static constexpr int kRowBytes = cache_row_bytes<FMT>(D);
+  // tensor memory: scores of kBufs tiles, O, Q and its bf16 form
+  static constexpr int kBufs = D == 64 ? 3 : 2;
+  static constexpr uint32_t kColO = 128 * kBufs, kColQ = kColO + D, kColQb = kColQ + D / 2;
+  static_assert(kColQb + D / 2 <= kTmemCols, "tensor memory");
   static constexpr int kChunks = kRowBytes / 16;       // per row
   static constexpr int kTileChunks = TK * kChunks;     // 16-byte chunks of a tile of bf16 rows
   static constexpr int kTileBytes = TK * D * 2;        // a bf16 tile
@@ -409,9 +418,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
       mbar_init(&bars[kVFull + b], kFillWarps);
       mbar_init(&bars[kKFree + b], 1);
       mbar_init(&bars[kVFree + b], 1);
-      mbar_init(&bars[kSFull + b], 1);
       mbar_init(&bars[kPReady + b], kSoftmaxWarps / 2);
     }
+    for (int b = 0; b < 3; ++b) mbar_init(&bars[kSFull + b], 1);
     mbar_init(&bars[kPvDone], 1);
     mbar_init(&bars[kQReady], kSoftmaxWarps);
     mbar_init(&bars[kODone], 1);
@@ -457,14 +466,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
           tc_fence_after();
           const uint64_t dk = smem_desc_sw128(sbase + (t & 1) * C::kTileBytes, 0, 1024);
           const bool half = C::kMx && !s_wide[t % kFlags];
-          const uint32_t qa = tmem + (half || !C::kMx ? kColQ : kColQb);
+          const uint32_t qa = tmem + (half || !C::kMx ? C::kColQ : C::kColQb);
           const uint32_t desc = half ? C::kIdescS & ~C::kBf16Types : C::kIdescS;
   #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             if (issuer)
-              mma_ts(tmem + 128 * (t & 1), qa + 8 * k, dk + (uint64_t)(((k / 4) * kBoxBytes + (k % 4) * 32) >> 4), desc, k > 0);
+              mma_ts(tmem + 128 * (t % C::kBufs), qa + 8 * k, dk + (uint64_t)(((k / 4) * kBoxBytes + (k % 4) * 32) >> 4), desc, k > 0);
           if (issuer) {
-            mma_commit(&bars[kSFull + (t & 1)]);
+            mma_commit(&bars[kSFull + t % C::kBufs]);
             mma_commit(&bars[kKFree + (t & 1)]);
           }
           return true;
@@ -472,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
         if (!(ok = (wait_bar(&bars[kQReady], (uint32_t)(parts & 1), wd)))) break;
         tc_fence_after();
         ok = issue_s(t0);
-        if (ok && n_tiles > 1) ok = issue_s(t0 + 1);
+        for (int n = 1; ok && n < C::kBufs && n < n_tiles; ++n) ok = issue_s(t0 + n);
         for (int n = 0; ok && n < n_tiles; ++n) {
           const int t = t0 + n;
           if (!(ok = (wait_bar(&bars[kVFull + (t & 1)], (uint32_t)(t >> 1 & 1), wd)))) break;
@@ -483,14 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
   #pragma unroll
           for (int k = 0; k < TK / 16; ++k)
             if (issuer)
-              mma_ts(tmem + kColO, tmem + 128 * (t & 1) + 64 * (k / 4) + 8 * (k % 4), dv + (uint64_t)((k * 16 * 128) >> 4),
+              mma_ts(tmem + C::kColO, tmem + 128 * (t % C::kBufs) + 64 * (k / 4) + 8 * (k % 4), dv + (uint64_t)((k * 16 * 128) >> 4),
                      desc, !(n == 0 && k == 0));
           if (issuer) {
             mma_commit(&bars[kPvDone]);
             mma_commit(&bars[kVFree + (t & 1)]);
             if (n + 1 == n_tiles) mma_commit(&bars[kODone]);
           }
-          if (n + 2 < n_tiles && !(ok = issue_s(t + 2))) break;
+          if (n + C::kBufs < n_tiles && !(ok = issue_s(t + C::kBufs))) break;
         }
         t0 += n_tiles;
         ++parts;
@@ -646,15 +655,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
 #pragma unroll
           for (int e = 0; e < D / 4; ++e)
             x[e] = pack_f16x2(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xffff0000u) * up);
-          put(kColQ);
+          put(C::kColQ);
 #pragma unroll
           for (int e = 0; e < D / 4; ++e) {  // (exact: 8 significant bits)
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
             x[e] = pack_bf16x2(f.x, f.y);
           }
-          put(kColQb);
+          put(C::kColQb);
         } else {
-          put(kColQ);
+          put(C::kColQ);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -676,9 +685,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
         // every row sees the whole tile
         const bool whole = kb + TK <= ks.n &&
                            (p.window <= 0 || kb + TK <= p.sinks || kb >= ks.n + p.T - p.window);
-        if (!(ok = (wait_bar(&bars[kSFull + hh], (uint32_t)(t >> 1 & 1), wd)))) break;
+        if (!(ok = (wait_bar(&bars[kSFull + t % C::kBufs], (uint32_t)(t / C::kBufs & 1), wd)))) break;
         tc_fence_after();
-        const uint32_t tS = tmem + lane_off + 128 * hh;
+        const uint32_t tS = tmem + lane_off + 128 * (t % C::kBufs);
         if (__builtin_expect(!whole, 0)) {
           // hidden scores are overwritten in place, by a loop: the straight path below stays
           // short (what the roles share is the instruction caches)
@@ -730,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
           // S of this tile was issued before the last P V: O must hold every product so far
           if (!(ok = (wait_bar(&bars[kPvDone], (uint32_t)((t - 1) & 1), wd)))) break;
           tc_fence_after();
-          rescale_o<D>(tmem + lane_off + kColO, !moved ? 1.f : (before == -INFINITY ? 0.f : ex2_approx(before - now)));
+          rescale_o<D>(tmem + lane_off + C::kColO, !moved ? 1.f : (before == -INFINITY ? 0.f : ex2_approx(before - now)));
         }
         const float sub = m == -INFINITY ? 0.f : m - C::kLift;
         // (the last columns are still in registers: they go first)
@@ -771,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         uint32_t o[32];
-        tmem_ld32(tmem + lane_off + kColO + hh * (D / 2) + 32 * c, o);
+        tmem_ld32(tmem + lane_off + C::kColO + hh * (D / 2) + 32 * c, o);
         tmem_wait_ld();
         if (live) {
           float v[32];
