@@ -307,7 +307,7 @@ def window_attention(q, k, v, window: int, sinks: int = 0, scale: float | None =
     lse = _like(lse, dev, "lse", (B, Hq, S), torch.float32)
     workspace = _scratch(workspace, 256, dev)
     rc = _call_on(dev, _b.ring_attn_window_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                  lse.data_ptr(), B, Hq, k.shape[1], S, D, int(window), int(sinks), scale, workspace.data_ptr(),
+                  lse.data_ptr(), B, Hq, k.shape[1], S, D, min(int(window), S), min(int(sinks), S), scale, workspace.data_ptr(),
                   workspace.nbytes, _stream_on(stream, dev))
     _b.check(rc, "ring_attn_window_fwd")
     return out, lse
@@ -330,7 +330,7 @@ def window_attention_backward(q, k, v, out, lse, dout, window: int, sinks: int =
     dev = q.device
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if workspace is None:
-        need = _b.ring_attn_window_bwd_workspace_bytes(B, Hq, k.shape[1], S, D, int(window), int(sinks))
+        need = _b.ring_attn_window_bwd_workspace_bytes(B, Hq, k.shape[1], S, D, min(int(window), S), min(int(sinks), S))
         if need == 0:
             raise _b.RingAttnError(_b.EINVAL, "ring_attn_window_bwd_workspace_bytes")
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -338,7 +338,7 @@ def window_attention_backward(q, k, v, out, lse, dout, window: int, sinks: int =
         workspace = _scratch(workspace, 0, dev)
     rc = _call_on(dev, _b.ring_attn_window_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                   lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, k.shape[1], S, D,
-                  int(window), int(sinks), scale, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
+                  min(int(window), S), min(int(sinks), S), scale, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
     _b.check(rc, "ring_attn_window_bwd")
     return dq, dk, dv
 

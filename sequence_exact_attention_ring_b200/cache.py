@@ -97,6 +97,11 @@ def _strides(t):
     return s0 if n0 > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0
 
 
+def _int31(x) -> int:
+    """x for a C int in which everything past the largest sequence, or below 0, means the same."""
+    return max(-1, min(int(x), 2 ** 31 - 1))
+
+
 def _on_device(cache: KVCache):
     dev = cache.k.device
     if dev.type != "cuda":
@@ -199,6 +204,6 @@ def tree_attention(q, cache: KVCache, lengths, parents=None, counts=None, window
     workspace = tree_workspace(q, cache) if workspace is None else _scratch(workspace, 0, dev)
     rc = _call_on(dev, _b.ring_attn_tree, q.data_ptr(), _strides(q), *cache._pointers(), _FORMATS[cache.format],
                   out.data_ptr(), lse.data_ptr(), B, Hq, cache.Hkv, cache.capacity, D, T, p_len, p_par, p_cnt,
-                  int(window), int(sinks), scale, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
+                  _int31(window), _int31(sinks), scale, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
     _b.check(rc, "ring_attn_tree")
     return out, lse

@@ -15,7 +15,7 @@ import torch
 
 import oracle
 from sequence_exact_attention_ring_b200 import (KVCache, RingAttnError, binding, cache_read, cache_write, merge, status,
-                                                tree_attention, tree_workspace)
+                                                tree_attention, tree_workspace, window_attention)
 
 pytestmark = pytest.mark.gpu
 
@@ -170,6 +170,109 @@ def test_large_scores_and_far_scales(cuda_lib):
         q = (8 * torch.randn(1, 4, 2, 128, generator=g)).bfloat16().cuda()
         run(q, cache, vals, [90], what=f"{fmt} mixed scales", floor=0.0)
         run(q, cache, vals, [4], what=f"{fmt} mixed scales, short", floor=0.0)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_and_far_scales(cuda_lib, fmt, D):
+    """Tiles of every mix: ordinary, blocks of zeros, K or V scales past fp16's range, 2^-40 to 2^40 in one tile,
+    scores that rise from tile to tile."""
+    g = torch.Generator().manual_seed(43)
+    n, T = 900, 20
+    cache = KVCache.allocate(1, 1, n + T + 12, D, fmt)
+    k, v = torch.randn(1, 1, n + T, D, generator=g), torch.randn(1, 1, n + T, D, generator=g)
+    k[0, 0, 130:250], v[0, 0, 140:384] = 0.0, 0.0                  # zero blocks, a V tile of zeros alone
+    k[0, 0, 260:270] *= 2.0 ** -30                                  # a K tile below the range
+    v[0, 0, 400:405] *= 2.0 ** 20                                   # a V tile above it, weights small
+    k[0, 0, 400:405] = 0.0
+    v[0, 0, 520:640] *= torch.exp2(torch.arange(120.0) / 3 - 40)[:, None]
+    k[0, 0, 530, 32:] *= 2.0 ** -60
+    k[0, 0, 640:] *= torch.linspace(0.5, 4, n + T - 640)[:, None]   # rising maxima
+    cache_write(cache, k.cuda(), v.cuda(), i32([0]))
+    vals = [t.double().cpu().numpy() for t in cache_read(cache, i32([0]), cache.capacity, dtype=torch.float32)]
+    q = (3 * torch.randn(1, 6, T, D, generator=g)).bfloat16().cuda()
+    run(q, cache, vals, [n], random_tree(1, T, 8), what="tree")
+    run(q, cache, vals, [n], window=300, sinks=150, what="window")
+    run(q, cache, vals, [0], what="drafts alone")
+    run(q[:, :, :1].expand(1, 6, 1, D)[:, :2], cache, vals, [n + T - 1], what="one token")
+
+
+def test_window_prefill_then_decode(cuda_lib):
+    """A windowed layer's prompt, its rows written to a cache, and its last tokens again as a chain over
+    the cache: the rows of the whole prompt's attention."""
+    B, Hq, Hkv, D, S, W, sinks = 2, 8, 2, 128, 700, 200, 5
+    g = torch.Generator().manual_seed(97)
+    q, k, v = (torch.randn(B, h, S, D, generator=g).bfloat16().cuda() for h in (Hq, Hkv, Hkv))
+    out, lse = window_attention(q, k, v, W, sinks)
+    O, L, A, E = oracle.window_reference(*(x.double().cpu().numpy() for x in (q, k, v)), W, sinks, D ** -0.5)
+    check(out, lse, (O, L, A, E), D, "prompt")
+    cache = KVCache.allocate(B, Hkv, S, D, "bf16")
+    cache_write(cache, k, v, i32([0] * B))
+    for T in (1, 3, 64):
+        o, l = tree_attention(q[:, :, S - T:], cache, i32([S - T] * B), window=W, sinks=sinks)
+        check(o, l, tuple(x[:, :, S - T:] for x in (O, L, A, E)), D, f"last {T}")
+
+
+def test_other_streams_and_two_at_once(cuda_lib):
+    """Calls follow the stream they are given, and two of them with their own workspaces do not meet."""
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for T, rep in ((1, 4), (9, 8)):
+        q, cache, vals = make(2, 2 * rep, 2, 128, T, [5000, 300], "mxfp8", 45)
+        n = i32([5000, 300])
+        want = tree_attention(q, cache, n)
+        got = []
+        torch.cuda.synchronize()
+        for s in (a, b):
+            ws = tree_workspace(q, cache)
+            late, len_late = torch.zeros_like(q), torch.zeros_like(n)
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(2_000_000)  # the inputs come late on the call's own stream
+                late.copy_(q)
+                len_late.copy_(n)
+            got += [tree_attention(late, cache, len_late, workspace=ws, stream=s, out=torch.empty_like(want[0]),
+                                   lse=torch.empty_like(want[1])) for _ in range(3)]
+        torch.cuda.synchronize()
+        for o, l in got:
+            assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+
+
+def test_two_graphs_with_one_workspace(cuda_lib):
+    """Captured calls of different shapes that share a workspace, replayed in any order on one stream."""
+    s = torch.cuda.Stream()
+    cases, ws = [], None
+    for T, rep, fmt in ((1, 4, "mxfp8"), (30, 8, "mxfp4")):
+        q, cache, vals = make(2, 2 * rep, 2, 64, T, [3000, 1700], fmt, 46)
+        n = i32([3000, 1700])
+        x = tree_workspace(q, cache)
+        ws = x if ws is None or x.nbytes > ws.nbytes else ws
+        cases.append([q, cache, n, tree_attention(q, cache, n)])
+    torch.cuda.synchronize()
+    for c in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+            got = tree_attention(c[0], c[1], c[2], workspace=ws)
+        c += [graph, got]
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        for t in cases[i][5]:
+            t.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            cases[i][4].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(cases[i][5][0], cases[i][3][0]) and torch.equal(cases[i][5][1], cases[i][3][1])
+
+
+def test_windows_past_every_int(cuda_lib):
+    """A window or sinks too large for the sequence, or for a C int, hold all of it."""
+    for T in (1, 20):
+        q, cache, vals = make(1, 4, 2, 64, T, [200], "mxfp8", 47)
+        for kw in (dict(window=2 ** 31 - 1), dict(window=2 ** 32), dict(window=2 ** 40 + 1, sinks=2 ** 33),
+                   dict(window=1, sinks=2 ** 31 - 1)):
+            got = tree_attention(q, cache, i32([200]), **kw)
+            ref = oracle.tree_reference(q.double().cpu().numpy(), *vals, [200], None, None, kw["window"],
+                                        kw.get("sinks", 0), 1 / 8)
+            check(*got, ref, 64, str(kw), weight_floor(cache, vals, [200], T))
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
