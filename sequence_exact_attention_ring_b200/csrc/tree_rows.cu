@@ -1022,7 +1022,10 @@ struct TreePlan {
 };
 
 // More than 16 query rows per kv head go to the tcgen05 form, whose tile is 128 rows whatever
-// part of them is real; up to 16 the warp form.
+// part of them is real; up to 16 the warp form, which takes the cache once per 16 rows. 32
+// (sequence, head) pairs of 32k keys, us, warps / tiles, at 8, 16, 20 and 64 rows: e4m3, D = 128
+// 66 / 106, 91 / 107, 154 / 108, 291 / 113; e2m1, D = 64 43 / 80, 55 / 81, 90 / 81, 167 / 83;
+// bf16, D = 128 95 / 93, 92 / 94, 166 / 95, 293 / 99.
 TreePlan tree_plan(const CacheView& c, int Hq, int T) {
   TreePlan t;
   const int rows = T * (Hq / c.Hkv);
