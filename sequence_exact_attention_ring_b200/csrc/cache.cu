@@ -129,32 +129,38 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
   const T* src = static_cast<const T*>(w ? p.src[1] : p.src[0]) + run.b * (w ? p.stride[1][0] : p.stride[0][0]) +
                  run.h * (w ? p.stride[1][1] : p.stride[0][1]) + sub * 8;
   const int64_t stride = w ? p.stride[1][2] : p.stride[0][2];
-  const int64_t head_row = ((int64_t)run.b * p.Hkv + run.h) * p.capacity;
-  uint8_t* codes = w ? p.codes[1] : p.codes[0];
-  uint8_t* scale = w ? p.scale[1] : p.scale[0];
-  if (n > p.T && p.status && threadIdx.x == 0) atomicExch(p.status, RING_ATTN_EINVAL);
+  // the new rows whose place is inside the cache: [lo, hi)
+  const int64_t rows = n < p.T ? n : p.T;
+  const int64_t lo = start < 0 ? -start : 0, hi = rows < p.capacity - start ? rows : p.capacity - start;
+  if (p.status && threadIdx.x == 0 && (n > p.T || (rows > 0 && (lo > 0 || hi < rows)))) atomicExch(p.status, RING_ATTN_EINVAL);
+  const uint32_t i0 = run.first + threadIdx.x / kTpr;
+  const int64_t row0 = ((int64_t)run.b * p.Hkv + run.h) * p.capacity + start + i0;
+  uint8_t* codes = (w ? p.codes[1] : p.codes[0]) + row0 * cache_row_bytes<FMT>(D) + sub * (cache_row_bytes<FMT>(D) / kTpr);
+  uint8_t* scale = (w ? p.scale[1] : p.scale[0]) + row0 * (D / kMxBlock) + sub / 4;
   Eight<T> x[kRows];
-  int64_t dst[kRows];
+  bool live[kRows];
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    const uint32_t i = run.first + u * rpb + threadIdx.x / kTpr;
-    dst[u] = -1;
+    const uint32_t i = i0 + u * rpb;
     x[u].clear();
-    if (i >= (uint32_t)p.T || (int32_t)i >= n) continue;
-    const int64_t pos = start + i;
-    const int64_t from = p.index ? (int64_t)p.index[(int64_t)run.b * p.T + i] : (int64_t)i;
-    if (pos < 0 || pos >= p.capacity || from < 0 || from >= p.T_src) {
-      if (p.status && sub == 0) atomicExch(p.status, RING_ATTN_EINVAL);
-      continue;
+    live[u] = i >= lo && i < hi;
+    if (!live[u]) continue;
+    int64_t from = i;
+    if (p.index) {
+      from = p.index[(int64_t)run.b * p.T + i];
+      if (from < 0 || from >= p.T_src) {
+        if (p.status && sub == 0) atomicExch(p.status, RING_ATTN_EINVAL);
+        live[u] = false;
+        continue;
+      }
     }
     x[u].load(src + from * stride);
-    dst[u] = head_row + pos;
   }
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     float y[8];
     if (FMT == RING_ATTN_CACHE_BF16) {
-      if (dst[u] < 0) continue;
+      if (!live[u]) continue;
       uint4 o;
       if constexpr (sizeof(T) == 2) {
         o = x[u].w;
@@ -162,27 +168,23 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
         x[u].scaled(1.f, y);
         o = make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(y[4], y[5]), bf16_pair(y[6], y[7]));
       }
-      *reinterpret_cast<uint4*>(codes + dst[u] * (2 * D) + sub * 16) = o;
+      *reinterpret_cast<uint4*>(codes + u * rpb * (2 * D)) = o;
       continue;
     }
     uint32_t m = x[u].amax();
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    if (dst[u] < 0) continue;
+    if (!live[u]) continue;
     const uint32_t byte = mx_scale_byte<FMT>(m);
     const bool finite = byte != 255u;  // the codes of a block that is not finite are zeros
     x[u].scaled(mx_inverse_scale(byte), y);
     if (FMT == RING_ATTN_CACHE_MXFP8) {
-      uint2 o;
-      o.x = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
-      o.y = e4m3_pair(y[4], y[5]) | (e4m3_pair(y[6], y[7]) << 16);
-      *reinterpret_cast<uint2*>(codes + dst[u] * D + sub * 8) = finite ? o : make_uint2(0u, 0u);
+      const uint2 o = make_uint2(e4m3_quad(y[0], y[1], y[2], y[3]), e4m3_quad(y[4], y[5], y[6], y[7]));
+      *reinterpret_cast<uint2*>(codes + u * rpb * D) = finite ? o : make_uint2(0u, 0u);
     } else {
-      const uint32_t o = e2m1_pair(y[0], y[1]) | (e2m1_pair(y[2], y[3]) << 8) | (e2m1_pair(y[4], y[5]) << 16) |
-                         (e2m1_pair(y[6], y[7]) << 24);
-      *reinterpret_cast<uint32_t*>(codes + dst[u] * (D / 2) + sub * 4) = finite ? o : 0u;
+      *reinterpret_cast<uint32_t*>(codes + u * rpb * (D / 2)) = finite ? e2m1_eight(y) : 0u;
     }
-    if (sub % 4 == 0) scale[dst[u] * (D / kMxBlock) + sub / 4] = (uint8_t)byte;
+    if (sub % 4 == 0) scale[u * rpb * (D / kMxBlock)] = (uint8_t)byte;
   }
 }
 

@@ -51,12 +51,24 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
                     : (byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23));
 }
 
-// Two values to two codes: e4m3 in 16 bits, e2m1 in 8 (first value low).
-__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+// Four values to four e4m3 codes, eight to eight e2m1 codes, the first value lowest; to
+// nearest even, larger magnitudes to the largest code.
+__device__ __forceinline__ uint32_t e4m3_quad(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
-__device__ __forceinline__ uint32_t e2m1_pair(float a, float b) {
-  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(a, b), __NV_E2M1, cudaRoundNearest);
+__device__ __forceinline__ uint32_t e2m1_eight(const float (&y)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return r;
 }
 __device__ __forceinline__ float2 e4m3_values(uint32_t codes) {
   const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3));
