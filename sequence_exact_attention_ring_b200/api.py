@@ -276,17 +276,32 @@ def _check_window(q, k, v, window, sinks):
         raise ValueError("window must be >= 1 and sinks >= 0")
 
 
-def _like(t, device, name, shape, dtype):
+def _new(like, shape, dtype):
+    if dtype == like.dtype and shape == like.shape:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    return like.new_empty(shape, dtype=dtype)
+
+
+def _like(t, like, name, shape, dtype, stream=None):
+    """t, or a new tensor of this shape on like's device, of `stream`'s own memory: what the current
+    stream has freed may still be in use there, and what `stream` uses must not be reused there."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        if stream is None:
+            return _new(like, shape, dtype)
+        with torch.cuda.stream(stream):
+            return _new(like, shape, dtype)
+    if t.shape != shape or t.dtype != dtype or t.device != like.device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the inputs' device")
     return t
 
 
-def _scratch(workspace, need, device):
+def _scratch(workspace, need, device, stream=None):
+    """workspace, or `need` bytes of `stream`'s own memory."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(stream):
+            return torch.empty(need, dtype=torch.uint8, device=device)
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     return workspace
@@ -303,9 +318,9 @@ def window_attention(q, k, v, window: int, sinks: int = 0, scale: float | None =
     B, Hq, S, D = q.shape
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     dev = q.device
-    out = _like(out, dev, "out", (B, Hq, S, D), torch.bfloat16)
-    lse = _like(lse, dev, "lse", (B, Hq, S), torch.float32)
-    workspace = _scratch(workspace, 256, dev)
+    out = _like(out, q, "out", (B, Hq, S, D), torch.bfloat16, stream)
+    lse = _like(lse, q, "lse", (B, Hq, S), torch.float32, stream)
+    workspace = _scratch(workspace, 256, dev, stream)
     rc = _call_on(dev, _b.ring_attn_window_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                   lse.data_ptr(), B, Hq, k.shape[1], S, D, min(int(window), S), min(int(sinks), S), scale, workspace.data_ptr(),
                   workspace.nbytes, _stream_on(stream, dev))
@@ -328,14 +343,14 @@ def window_attention_backward(q, k, v, out, lse, dout, window: int, sinks: int =
         raise ValueError("lse must be a contiguous float32 [B, Hq, S] tensor")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     dev = q.device
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dq, dk, dv = (_like(None, t, "", t.shape, t.dtype, stream) for t in (q, k, v))
     if workspace is None:
         need = _b.ring_attn_window_bwd_workspace_bytes(B, Hq, k.shape[1], S, D, min(int(window), S), min(int(sinks), S))
         if need == 0:
             raise _b.RingAttnError(_b.EINVAL, "ring_attn_window_bwd_workspace_bytes")
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
-        workspace = _scratch(workspace, 0, dev)
+        need = 0
+    workspace = _scratch(workspace, need, dev, stream)
     rc = _call_on(dev, _b.ring_attn_window_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                   lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, k.shape[1], S, D,
                   min(int(window), S), min(int(sinks), S), scale, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))

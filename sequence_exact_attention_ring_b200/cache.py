@@ -154,8 +154,8 @@ def cache_read(cache: KVCache, start, T: int, count=None, dtype=torch.bfloat16, 
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float32 or bfloat16")
     shape = (cache.B, cache.Hkv, T, cache.D)
-    k_out = _like(k_out, dev, "k_out", shape, dtype)
-    v_out = _like(v_out, dev, "v_out", shape, dtype)
+    k_out = _like(k_out, cache.k, "k_out", shape, dtype, stream)
+    v_out = _like(v_out, cache.k, "v_out", shape, dtype, stream)
     if T == 0:
         return k_out, v_out
     p_start = _int_rows(_required(start, "start"), (cache.B,), "start", dev)
@@ -167,13 +167,17 @@ def cache_read(cache: KVCache, start, T: int, count=None, dtype=torch.bfloat16, 
     return k_out, v_out
 
 
-def tree_workspace(q, cache: KVCache) -> torch.Tensor:
-    """Scratch for tree_attention calls of q's shape over this cache (one call at a time)."""
+def _tree_bytes(q, cache: KVCache) -> int:
     B, Hq, T, D = q.shape
     n = _b.ring_attn_tree_workspace_bytes(_FORMATS[cache.format], B, Hq, cache.Hkv, cache.capacity, D, T)
     if n == 0:
         raise _b.RingAttnError(_b.EINVAL, "ring_attn_tree_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=cache.k.device)
+    return n
+
+
+def tree_workspace(q, cache: KVCache) -> torch.Tensor:
+    """Scratch for tree_attention calls of q's shape over this cache (one call at a time)."""
+    return _scratch(None, _tree_bytes(q, cache), cache.k.device)
 
 
 def tree_attention(q, cache: KVCache, lengths, parents=None, counts=None, window: int = 0, sinks: int = 0,
@@ -196,12 +200,12 @@ def tree_attention(q, cache: KVCache, lengths, parents=None, counts=None, window
         raise ValueError("q must be a bf16 tensor on the cache's device with a contiguous head dimension")
     B, Hq, T, D = q.shape
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    out = _like(out, dev, "out", (B, Hq, T, D), torch.bfloat16)
-    lse = _like(lse, dev, "lse", (B, Hq, T), torch.float32)
+    out = _like(out, q, "out", (B, Hq, T, D), torch.bfloat16, stream)
+    lse = _like(lse, q, "lse", (B, Hq, T), torch.float32, stream)
     p_len = _int_rows(_required(lengths, "lengths"), (B,), "lengths", dev)
     p_par = _int_rows(parents, (B, T), "parents", dev)
     p_cnt = _int_rows(counts, (B,), "counts", dev)
-    workspace = tree_workspace(q, cache) if workspace is None else _scratch(workspace, 0, dev)
+    workspace = _scratch(workspace, _tree_bytes(q, cache) if workspace is None else 0, dev, stream)
     rc = _call_on(dev, _b.ring_attn_tree, q.data_ptr(), _strides(q), *cache._pointers(), _FORMATS[cache.format],
                   out.data_ptr(), lse.data_ptr(), B, Hq, cache.Hkv, cache.capacity, D, T, p_len, p_par, p_cnt,
                   _int31(window), _int31(sinks), scale, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))

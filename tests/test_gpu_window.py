@@ -10,8 +10,8 @@ import pytest
 import torch
 
 import oracle
-from sequence_exact_attention_ring_b200 import (RingAttnError, binding, ring_attention, status, window_attention,
-                                                window_attention_backward)
+from sequence_exact_attention_ring_b200 import (KVCache, RingAttnError, binding, cache_read, cache_write, ring_attention,
+                                                status, tree_attention, window_attention, window_attention_backward)
 from test_gpu_tree import check
 
 pytestmark = pytest.mark.gpu
@@ -221,3 +221,49 @@ def test_refusals(cuda_lib):
     with pytest.raises(RingAttnError) as e:
         window_attention_backward(q, k, v, out, lse, do, 8, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.code == binding.EWORKSPACE
+
+
+@pytest.mark.parametrize("what", ["window", "gradients", "tree", "read"])
+def test_memory_of_a_call_on_another_stream_is_not_reused_early(cuda_lib, what):
+    """A call on a given stream still runs when it returns: the scratch and outputs that it allocated must
+    not be handed to the current stream's next tensors meanwhile."""
+    q, k, v, do = inputs(1, 4, 2, 3000, 128, 19)
+    out, lse = window_attention(q, k, v, 200, 4)
+    cache = KVCache.allocate(1, 2, 3000, 128, "bf16")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache_write(cache, k, v, zero)
+    length = zero + 2991
+    calls = dict(window=lambda s: window_attention(q, k, v, 200, 4, stream=s),
+                 gradients=lambda s: window_attention_backward(q, k, v, out, lse, do, 200, 4, stream=s),
+                 tree=lambda s: tree_attention(q[:, :, :9], cache, length, stream=s),
+                 read=lambda s: cache_read(cache, zero, 3000, stream=s))
+    want = [t.clone() for t in calls[what](None)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+    got = calls[what](s)
+    kept = []
+    sizes = [256, 1 << 12, 1 << 16, 1 << 20] + [t.nbytes for t in got] + [1 << 24, 1 << 25]
+    for n in sizes * 3:
+        kept.append(torch.full((n,), 0x5a, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert all((t == 0x5a).all() for t in kept)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # and dropped at once, outputs and all
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+    del got
+    calls[what](s)
+    kept = [torch.full((n,), 0x5a, dtype=torch.uint8, device="cuda") for n in sizes * 3]
+    torch.cuda.synchronize()
+    assert all((t == 0x5a).all() for t in kept)
+    # what the current stream has freed is still read there
+    old = [torch.full((n,), 0x5a, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    copies = [t.clone() for t in old]
+    del old
+    calls[what](s)
+    torch.cuda.synchronize()
+    assert all((t == 0x5a).all() for t in copies)
