@@ -102,14 +102,18 @@ struct CfgB {  // dq
   static constexpr int kSlotBytes = 2 * kStepTileBytes;
   static constexpr int kSlots = 6;
   static constexpr int kOffBar = kSlots * kSlotBytes;
-  static constexpr int kNumBars = 7 + 2 * kSlots;
+  static constexpr int kNumBars = 8 + 2 * kSlots;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
   static_assert(kSlots >= 3, "steps n, n + 1 and n + 2 are held at once");
   static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
   static constexpr uint32_t kIdescTS = idesc_bf16_f32(BT, D, 0, 1);
+  // Q and dO wait in the ring's last two slots for the warps that take them to tensor memory
+  static constexpr int kSlotQ = kSlots - 2, kSlotDO = kSlots - 1;
+  static constexpr int kTileBytes = BT * D * 2;
+  static_assert(kTileBytes <= kSlotBytes, "a tile of queries fits a slot");
 };
-enum BarB { kB_QReady = 0, kB_SFull = 1, kB_PReady = 3, kB_Done = 5, kB_Drain = 6, kB_Ring = 7 };
+enum BarB { kB_QReady = 0, kB_SFull = 1, kB_PReady = 3, kB_Done = 5, kB_Drain = 6, kB_QFull = 7, kB_Ring = 8 };
 
 // How the key tiles are divided. Tiles [0, sink_tiles) are seen by every later query: their
 // query steps are cut into `segs` runs. Every tile's query heads are cut into `splits`
@@ -125,8 +129,6 @@ struct Plan {
 struct Params {
   WinGeom g;
   Plan plan;
-  const uint16_t* q;
-  const uint16_t* dout;
   const float* nlse2;  // [B*Hq][s_pad]: -lse log2 e
   const float* ndelta; // -Delta
   int64_t s_pad;
@@ -587,8 +589,8 @@ __global__ void __launch_bounds__(256) window_reduce_kernel(const __grid_constan
 
 // ---------------------------------------------------------------------------------- dQ
 template <int D>
-__device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p,
-                                        uint8_t* smem, int64_t u) {
+__device__ __forceinline__ void dq_unit(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtensorMap& tm_k,
+                                        const CUtensorMap& tm_v, const Params& p, uint8_t* smem, int64_t u) {
   using C = CfgB<D>;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -609,32 +611,6 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorM
   const int bh_q = bh_kv * rep + hr;
   const WinTiles wt = win_tiles(g, a0, a0 + BT - 1, TS);
   const int N = win_count(wt);
-  // The elementwise warps' rows of Q and dO, dims (D/2) hh .. as bf16 pairs (the memory order;
-  // rows past the sequence are zeros), and statistics: asked for before all else.
-  uint32_t rows[2][D / 4];
-  float row_nlse2 = 0.f, row_ndelta = 0.f;
-  if (warp < kEwWarps) {
-    const int64_t a = a0 + (warp % 4) * 32 + lane;
-    const bool row_ok = a < g.S;
-    const int64_t base = ((int64_t)bh_q * g.S + (row_ok ? a : 0)) * D + (D / 2) * (warp / 4);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint16_t* src = (t == 0 ? p.q : p.dout) + base;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const uint4 v4 = row_ok ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-        rows[t][4 * c] = v4.x;
-        rows[t][4 * c + 1] = v4.y;
-        rows[t][4 * c + 2] = v4.z;
-        rows[t][4 * c + 3] = v4.w;
-      }
-    }
-    grid_wait();
-    const int64_t stat = (int64_t)bh_q * p.s_pad + a;  // a < s_pad always
-    row_nlse2 = p.nlse2[stat];
-    row_ndelta = p.ndelta[stat];
-  }
-
   if (threadIdx.x == 0) {
     mbar_init(&bars[kB_QReady], kEwWarps);
     for (int b = 0; b < 2; ++b) {
@@ -643,6 +619,7 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorM
     }
     mbar_init(&bars[kB_Done], 1);
     mbar_init(&bars[kB_Drain], 1);
+    mbar_init(&bars[kB_QFull], 1);
     for (int s = 0; s < 2 * C::kSlots; ++s) mbar_init(&bars[kB_Ring + s], 1);
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -661,13 +638,20 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorM
 
   if (warp == kProducerWarp) {
     if (lane == 0 && N > 0) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
+      mbar_arrive_expect_tx(&bars[kB_QFull], 2 * C::kTileBytes);
+      for (int t = 0; t < 2; ++t) {
+        uint8_t* dst = smem + (t == 0 ? C::kSlotQ : C::kSlotDO) * C::kSlotBytes;
+        for (int bx = 0; bx < D / BOXW; ++bx)
+          for (int r = 0; r < BT; r += TS)
+            tma_load_4d(dst + bx * kBoxBytes + r * 128, t == 0 ? &tm_q : &tm_do, &bars[kB_QFull], bx * BOXW, (int)a0 + r, 0,
+                        bh_q);
+      }
       int m = 0;
       bool ok = true;
       for (; m < N; ++m) {
         const int slot = slot_of(m);
         const int row = win_tile(wt, m) * TS;
+        if (m == C::kSlotQ && !(ok = mbar_wait_backoff<false>(&bars[kB_QReady], 0, wd, kProducerSleepNs))) break;
         if (!(ok = mbar_wait_backoff<false>(&empty[slot], phase_of(m) ^ 1, wd, kProducerSleepNs))) break;
         uint8_t* dst = smem + slot * C::kSlotBytes;
         mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
@@ -677,6 +661,7 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorM
           tma_load_4d(dst + C::kStepTileBytes + bx * kStepBoxBytes, &tm_v, &full[slot], bx * BOXW, row, 0, bh_kv);
       }
       if (!ok) {
+        drain_wait(&bars[kB_QFull], 0, p.watchdog_ns);
         for (int x = (m > C::kSlots ? m - C::kSlots : 0); x < m; ++x)
           drain_wait(&full[slot_of(x)], phase_of(x), p.watchdog_ns);
       }
@@ -732,22 +717,41 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_k, const CUtensorM
     const int64_t a = a0 + wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const bool row_ok = a < g.S;
-    {
+    grid_wait();
+    const int64_t stat = (int64_t)bh_q * p.s_pad + a;  // a < s_pad always
+    const float row_nlse2 = p.nlse2[stat];
+    const float row_ndelta = p.ndelta[stat];
+    bool ok = N > 0 && mbar_wait(&bars[kB_QFull], 0, wd);
+    if (ok) {
+      // this thread's row of Q and dO, dims (D/2) hh .., as bf16 pairs (the memory order; rows
+      // past the sequence are zeros), from the swizzled tiles: row by row from global memory the
+      // 16-byte loads of 32 rows each took 4000 clocks
+      const int r = wq * 32 + lane;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
+        const uint8_t* row = smem + (t == 0 ? C::kSlotQ : C::kSlotDO) * C::kSlotBytes + (D == 128 ? hh * kBoxBytes : 0) + r * 128;
+        uint32_t x[D / 4];
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const int ch = D == 128 ? c : 4 * hh + c;
+          const uint4 v4 = *reinterpret_cast<const uint4*>(row + ((ch ^ (r & 7)) * 16));
+          x[4 * c] = v4.x;
+          x[4 * c + 1] = v4.y;
+          x[4 * c + 2] = v4.z;
+          x[4 * c + 3] = v4.w;
+        }
         const uint32_t dst = tmem + lane_off + (t == 0 ? kColQ : kColDO) + (D / 4) * hh;
         if constexpr (D == 128)
-          tmem_st32(dst, rows[t]);
+          tmem_st32(dst, x);
         else
-          tmem_st16(dst, rows[t]);
+          tmem_st16(dst, x);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kB_QReady]);
     }
-    bool ok = true;
-    for (int n = 0; n < N; ++n) {
+    for (int n = 0; ok && n < N; ++n) {
       const int b = n & 1;
       if (!(ok = mbar_wait(&bars[kB_SFull + b], (uint32_t)((n >> 1) & 1), wd))) break;
       tc_fence_after();
@@ -796,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x < p.plan.units)
     dkdv_unit<D>(tm_q64, tm_do64, tm_k, tm_v, p, smem, blockIdx.x);
   else
-    dq_unit<D>(tm_k64, tm_v64, p, smem, blockIdx.x - p.plan.units);
+    dq_unit<D>(tm_q64, tm_do64, tm_k64, tm_v64, p, smem, blockIdx.x - p.plan.units);
 }
 
 Plan make_plan(const WinGeom& g) {
@@ -839,8 +843,6 @@ int launch(const void* q, const void* k, const void* v, const void* out, const f
   Params p;
   p.g = g;
   p.plan = make_plan(g);
-  p.q = static_cast<const uint16_t*>(q);
-  p.dout = static_cast<const uint16_t*>(dout);
   p.nlse2 = scratch;
   p.ndelta = scratch + rows;
   p.s_pad = (g.S + BT - 1) / BT * BT;
