@@ -28,6 +28,12 @@
 // query, S / 64 steps instead of window / 64 + 3. Such a tile's queries are cut into parts
 // of a plain tile's length that run as CTAs of their own, and where the tiles alone do not
 // fill the GPU the heads of a group are divided among CTAs too.
+//
+// What bounds it: the products. At D = 128 a step of dkdv is 1280 clocks of them (the score
+// products read both operands from shared memory: 48 clocks each at N = 64, of 32 for the
+// multiplications) and takes 1500 to 1570, a step of dq 1024 and takes 1190; a CTA's start and
+// end, which nothing overlaps, take 6000 to 8000. 32k tokens, window 2048, 16 query heads over
+// 4: 2.11 ms, 669 TFLOP/s at 10 D flops a pair.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -37,6 +43,7 @@
 #include "sm100_ptx.cuh"
 #include "softmax_rows.cuh"
 #include "window_geom.h"
+#include "window_store.cuh"
 
 namespace ringattn {
 namespace winbwd {
@@ -472,8 +479,6 @@ __device__ __forceinline__ void dkdv_unit(const CUtensorMap& tm_q, const CUtenso
   } else if (warp < kEwWarps) {
     // warp = 4 hh + wq: TMEM lanes 32 wq (key rows), query columns 32 hh .. 32 hh + 31 of a step
     const int wq = warp % 4, hh = warp / 4;
-    const int r = wq * 32 + lane;
-    const int64_t u = U.kt * BT + r;  // this thread's key
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const int fr = lane / 4, fc = 2 * (lane % 4);  // fragment row, first column
     int64_t in0, in1;
@@ -528,14 +533,17 @@ __device__ __forceinline__ void dkdv_unit(const CUtensorMap& tm_q, const CUtenso
     if (have || N == 0) {
       tc_fence_after();
       const uint32_t tAcc = tmem + lane_off + kColAcc + hh * (D / 2);
+      // (every copy into the ring has been used: it is free)
+      uint8_t* stage = smem + C::kOffRing + warp * kStageBytesF32;
       if (U.part < 0) {
-        const bool row_ok = u < g.S;
-        const int64_t out_row = U.bh * g.S + (row_ok ? u : 0);
-        store_row_cols<D / 2>(tAcc, N > 0, row_ok, 1.f, false, p.dv, out_row, D, hh * (D / 2));
-        store_row_cols<D / 2>(tAcc + D, N > 0, row_ok, p.scale, false, p.dk, out_row, D, hh * (D / 2));
+        const int64_t first = U.kt * BT + wq * 32;
+        store_rows_staged<D / 2, false>(tAcc, N > 0, 1.f, stage, p.dv, U.bh * g.S + first, g.S - first, D, hh * (D / 2));
+        store_rows_staged<D / 2, false>(tAcc + D, N > 0, p.scale, stage, p.dk, U.bh * g.S + first, g.S - first, D,
+                                        hh * (D / 2));
       } else {
-        store_row_cols<D / 2>(tAcc, N > 0, true, 1.f, true, p.parts, U.part * 2 * BT + r, D, hh * (D / 2));
-        store_row_cols<D / 2>(tAcc + D, N > 0, true, p.scale, true, p.parts, U.part * 2 * BT + BT + r, D, hh * (D / 2));
+        const int64_t first = U.part * 2 * BT + wq * 32;
+        store_rows_staged<D / 2, true>(tAcc, N > 0, 1.f, stage, p.parts, first, 32, D, hh * (D / 2));
+        store_rows_staged<D / 2, true>(tAcc + D, N > 0, p.scale, stage, p.parts, first + BT, 32, D, hh * (D / 2));
       }
     }
   }
@@ -716,7 +724,6 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_q, const CUtensorM
     const int wq = warp % 4, hh = warp / 4;
     const int64_t a = a0 + wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    const bool row_ok = a < g.S;
     grid_wait();
     const int64_t stat = (int64_t)bh_q * p.s_pad + a;  // a < s_pad always
     const float row_nlse2 = p.nlse2[stat];
@@ -774,9 +781,10 @@ __device__ __forceinline__ void dq_unit(const CUtensorMap& tm_q, const CUtensorM
     }
     if (N > 0 && ok && mbar_wait(&bars[kB_Done], 0, wd)) {
       tc_fence_after();
-      const int64_t out_row = (int64_t)bh_q * g.S + (row_ok ? a : 0);
-      store_row_cols<D / 2>(tmem + lane_off + kColAcc + hh * (D / 2), true, row_ok, p.scale, false, p.dq, out_row, D,
-                            hh * (D / 2));
+      const int64_t first = a0 + wq * 32;
+      store_rows_staged<D / 2, false>(tmem + lane_off + kColAcc + hh * (D / 2), true, p.scale,
+                                      smem + warp * kStageBytesF32, p.dq, (int64_t)bh_q * g.S + first, g.S - first, D,
+                                      hh * (D / 2));
     }
   }
 
