@@ -362,6 +362,14 @@ __device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st_frag16_wide(uint32_t taddr, const uint32_t* r) {  // the same, stored
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 // 16 lanes x 16 columns: register 2 i + j of lane l goes to lane l / 4 + 8 j, column
 // 4 i + l % 4 (the fragment above with its pairs of columns packed to 16 bits each).
 __device__ __forceinline__ void tmem_st_frag16(uint32_t taddr, const uint32_t* r) {

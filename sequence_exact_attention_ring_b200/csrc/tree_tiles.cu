@@ -93,7 +93,7 @@ struct Cfg {
   static constexpr int kScaleRow = kMx ? D / kMxBlock : 0;
   static constexpr int kRawScale = 2 * TK * kRowBytes;
   static constexpr int kRawBytes = 2 * TK * (kRowBytes + kScaleRow);
-  static constexpr int kRawFit = kMx ? (kSmemLimit - 1024 - 2048 - kOffRaw - 512) / kRawBytes : 0;
+  static constexpr int kRawFit = kMx ? (kSmemLimit - 1024 - 2560 - kOffRaw - 512) / kRawBytes : 0;
   static constexpr int kRaw = kRawFit < kMaxRaw ? kRawFit : kMaxRaw;
   static_assert(!kMx || kRaw >= 2, "a tile is fetched while another is converted");
   // Converting: a task is 16 elements of one row, two 16-byte chunks out. Four lanes take the
@@ -104,8 +104,8 @@ struct Cfg {
   static constexpr int kRowStep = kFill / (4 * kBoxes);
   static constexpr int kPasses = TK / kRowStep;
   static_assert(kRowStep % 8 == 0 && TK % kRowStep == 0, "one swizzled position per thread");
-  static constexpr int kOffMax = kOffRaw + kRaw * kRawBytes;  // [2][2][128] floats
-  static constexpr int kOffBar = kOffMax + 2048;
+  static constexpr int kOffMax = kOffRaw + kRaw * kRawBytes;  // [5][128] floats
+  static constexpr int kOffBar = kOffMax + 2560;
   static constexpr int kSmemBytes = kOffBar + 512 + 1024;  // barriers, flags, alignment
   static_assert(kNumBars * 8 + 16 + 2 * kFlags <= 512, "barriers and flags");
   static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
@@ -606,6 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
     const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
     float* s_m = reinterpret_cast<float*>(smem + C::kOffMax);  // [t % 2][row]: the row's reference after tile t
     float* s_x = s_m + 256;                                    // [half][row]
+    float* s_scale = s_m + 512;                                // [row]: scores to the base-2 domain
     Walk walk = s_walk;
     Part part;
     int t0 = 0, parts = 0;
@@ -616,50 +617,50 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
       const int row = part.grp * TM + r;
       const bool live = row < ks.cnt * p.rep;
       const int node = live ? row / p.rep : 0;
-      float score_scale = p.scale_log2;
       {
-        // half a query row into tensor memory (with codes: in fp16, times 2^(14 - exponent of
-        // the row's largest element), and the same in bf16)
-        const uint16_t* src = p.q + part.b * p.qs_b + (int64_t)(part.kvh * p.rep + (live ? row % p.rep : 0)) * p.qs_h +
-                              node * p.qs_t;
-        uint32_t x[D / 4];
-        float up = 1.f;
-        if (C::kMx) {
-          uint32_t top = 0;
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = live ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        // Sixteen query rows into tensor memory, as fragments (four lanes side by side on a row: with
+        // a row per lane the loads' 32 lines each took 5000 clocks a part). With codes: in fp16,
+        // times 2^(14 - exponent of the row's largest element), and the same in bf16.
+        const int r16 = 32 * wq + 16 * hh;  // first of them
+        uint32_t x[D / 4], top[2] = {0, 0};  // registers as in tmem_ld_frag16, 32 words of a row after 32
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+        for (int j = 0; j < 2; ++j) {
+          const int mine = part.grp * TM + r16 + lane / 4 + 8 * j;
+          const bool in = mine < ks.cnt * p.rep;
+          const uint16_t* src = p.q + part.b * p.qs_b + (int64_t)(part.kvh * p.rep + (in ? mine % p.rep : 0)) * p.qs_h +
+                                (in ? mine / p.rep : 0) * p.qs_t + 4 * (lane % 4);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint2 v = in ? *reinterpret_cast<const uint2*>(src + 16 * i) : make_uint2(0u, 0u);
+            x[4 * i + 2 * j] = v.x;
+            x[4 * i + 2 * j + 1] = v.y;
+            top[j] = max(max(top[j], max(v.x & 0x7fffu, v.x >> 16 & 0x7fffu)), max(v.y & 0x7fffu, v.y >> 16 & 0x7fffu));
           }
-          const int e = max((int)(top >> 7), 15) - 127;  // not below 2^-112
-          up = pow2i(14 - e);
-          score_scale = p.scale_log2 * exp2f((float)(e - 14 - C::kBias));
-        }
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint4 v = live ? *reinterpret_cast<const uint4*>(src + hh * (D / 2) + 8 * c) : make_uint4(0, 0, 0, 0);
-          x[4 * c] = v.x;
-          x[4 * c + 1] = v.y;
-          x[4 * c + 2] = v.z;
-          x[4 * c + 3] = v.w;
         }
         auto put = [&](uint32_t col) {
-          if constexpr (D == 128)
-            tmem_st32(tmem + lane_off + col + 32 * hh, x);
-          else
-            tmem_st16(tmem + lane_off + col + 16 * hh, x);
+#pragma unroll
+          for (int w = 0; w < D / 64; ++w)
+            tmem_st_frag16_wide(tmem + ((uint32_t)r16 << 16) + col + 32 * w, x + 16 * w);
         };
         if (C::kMx) {
 #pragma unroll
-          for (int e = 0; e < D / 4; ++e)
-            x[e] = pack_f16x2(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xffff0000u) * up);
+          for (int j = 0; j < 2; ++j) {
+            top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 1));
+            top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 2));
+            const int e = max((int)(top[j] >> 7), 15) - 127;  // not below 2^-112
+            const float up = pow2i(14 - e);
+            if (lane % 4 == 0) s_scale[r16 + lane / 4 + 8 * j] = p.scale_log2 * exp2f((float)(e - 14 - C::kBias));
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int w = 4 * i + 2 * j; w < 4 * i + 2 * j + 2; ++w)
+                x[w] = pack_f16x2(__uint_as_float(x[w] << 16) * up, __uint_as_float(x[w] & 0xffff0000u) * up);
+          }
           put(C::kColQ);
 #pragma unroll
-          for (int e = 0; e < D / 4; ++e) {  // (exact: 8 significant bits)
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
-            x[e] = pack_bf16x2(f.x, f.y);
+          for (int w = 0; w < D / 4; ++w) {  // (exact: 8 significant bits)
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[w]));
+            x[w] = pack_bf16x2(f.x, f.y);
           }
           put(C::kColQb);
         } else {
@@ -668,13 +669,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kQReady]);
+        if (lane == 0) {
+          mbar_arrive(&bars[kQReady]);
+          mbar_arrive(&bars[kPair + wq]);
+        }
       }
       const Nodes nodes = warp_nodes(p, part.b, ks);
       uint64_t seen;
       int depth;
       node_of(nodes, node, seen, depth);
       const int lo_key = p.window > 0 ? ks.n + depth - p.window + 1 : 0;
+      // (the pair's barrier passes twice a part)
+      if (!(ok = (wait_bar(&bars[kPair + wq], 0, wd)))) break;
+      const float score_scale = C::kMx ? s_scale[r] : p.scale_log2;
       // this warp's part of the row's sum, relative to the reference m (a whole number) of its
       // last tile
       float m = -INFINITY, l = 0.f;
@@ -762,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
       s_m[hh * 128 + r] = m;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kPair + wq]);
-      if (!(ok = (wait_bar(&bars[kPair + wq], (uint32_t)(parts & 1), wd)))) break;
+      if (!(ok = (wait_bar(&bars[kPair + wq], 1, wd)))) break;
       const float m_other = s_m[(hh ^ 1) * 128 + r], l_other = s_x[(hh ^ 1) * 128 + r];
       const float m_row = fmaxf(m, m_other);
       l = m == -INFINITY ? 0.f : l * ex2_approx(m - m_row);
