@@ -783,34 +783,38 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
       const float inv = none ? 0.f : pow2i(-C::kBias) / L;  // O carries V's factor as well
       const float lse2 = none ? -INFINITY : m + log2f(L * (C::kMx ? 0x1p-9f : 1.f));
       const int64_t slot = (int64_t)blockIdx.x + part.unit;
-      const int64_t orow = live ? out_row(p, part.b, part.kvh, row) : 0;
+      // columns hh D/2 .. of this warp's rows, as fragments: four lanes side by side on a row
 #pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tmem + lane_off + C::kColO + hh * (D / 2) + 32 * c, o);
-        tmem_wait_ld();
-        if (live) {
-          float v[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * inv;
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
           const int d0 = hh * (D / 2) + 32 * c;
-          if (part.alone) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + d0);
+          uint32_t o[16];
+          tmem_ld_frag16(tmem + lane_off + ((uint32_t)t << 20) + C::kColO + d0, o);
+          tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              dst[e / 8] = make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
-                                      pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
-          } else {
-            float* dst = p.o_parts + (slot * TM + r) * D + d0;
+          for (int j = 0; j < 2; ++j) {
+            const int rr = 16 * t + 8 * j + lane / 4, at = part.grp * TM + 32 * wq + rr;
+            const float f = __shfl_sync(0xffffffffu, inv, rr);
+            if (at >= ks.cnt * p.rep) continue;
+            if (part.alone) {
+              uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + out_row(p, part.b, part.kvh, at) * D + d0) + lane % 4;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+              for (int i = 0; i < 4; ++i)
+                dst[4 * i] = pack_bf16x2(__uint_as_float(o[4 * i + 2 * j]) * f, __uint_as_float(o[4 * i + 2 * j + 1]) * f);
+            } else {
+              float* dst = p.o_parts + (slot * TM + 32 * wq + rr) * D + d0 + 2 * (lane % 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float2*>(dst + 8 * i) = make_float2(__uint_as_float(o[4 * i + 2 * j]) * f,
+                                                                      __uint_as_float(o[4 * i + 2 * j + 1]) * f);
+            }
           }
         }
       }
       if (live && hh == 0) {
         if (part.alone)
-          p.lse[orow] = lse2 * 0.69314718055994530942f;
+          p.lse[out_row(p, part.b, part.kvh, row)] = lse2 * 0.69314718055994530942f;
         else
           p.lse_parts[slot * TM + r] = lse2;
       }
