@@ -9,8 +9,8 @@
 // the group's rows is real), the exponentials (128 x 128 per tile at 16 a clock: as long as
 // the products at D = 128) and, with codes, their conversion. What bounds it as built is the
 // chain of one softmax warp (scores ready, maxima, reference, exponentials, P), 4400 clocks a
-// tile, of which two run at a time: 148 CTAs take 60 us for 12 groups of 116 rows and 50k keys
-// of e2m1 (D = 128, 17 us of products), 100 us for 128 full groups and 8k keys of e4m3 (D = 64,
+// tile, of which two run at a time: 148 CTAs take 51 us for 12 groups of 116 rows and 50k keys
+// of e2m1 (D = 128, 17 us of products), 96 us for 128 full groups and 8k keys of e4m3 (D = 64,
 // 21 us). The cache's rows are contiguous and come in as they are, by bulk copies into a ring of
 // raw tiles; eight warps convert them, 8 elements at a time, into the swizzled K and V tiles
 // that the products read. bf16 rows are copied straight into those tiles.
