@@ -72,8 +72,8 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxRaw = 4;
 constexpr int kFlags = 16;  // tiles whose form is remembered (more than are ever in flight)
 
-enum Bar { kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kPReady = 8, kPvDone = 10, kQReady = 11, kODone = 12,
-           kDrain = 13, kPair = 14, kMax = 18, kSFull = 26, kRawFull = 29, kRawFree = kRawFull + kMaxRaw,
+enum Bar { kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kPReady = 8, kQReady = 10, kODone = 11, kDrain = 12,
+           kPair = 13, kMax = 17, kSFull = 25, kPvDone = 28, kRawFull = 31, kRawFree = kRawFull + kMaxRaw,
            kRawSeen = kRawFree + kMaxRaw, kNumBars = kRawSeen + 2 * kMaxRaw };
 
 template <int FMT, int D>
@@ -420,8 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
       mbar_init(&bars[kVFree + b], 1);
       mbar_init(&bars[kPReady + b], kSoftmaxWarps / 2);
     }
-    for (int b = 0; b < 3; ++b) mbar_init(&bars[kSFull + b], 1);
-    mbar_init(&bars[kPvDone], 1);
+    for (int b = 0; b < 3; ++b) {
+      mbar_init(&bars[kSFull + b], 1);
+      mbar_init(&bars[kPvDone + b], 1);
+    }
     mbar_init(&bars[kQReady], kSoftmaxWarps);
     mbar_init(&bars[kODone], 1);
     mbar_init(&bars[kDrain], 1);
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
               mma_ts(tmem + C::kColO, tmem + 128 * (t % C::kBufs) + 64 * (k / 4) + 8 * (k % 4), dv + (uint64_t)((k * 16 * 128) >> 4),
                      desc, !(n == 0 && k == 0));
           if (issuer) {
-            mma_commit(&bars[kPvDone]);
+            mma_commit(&bars[kPvDone + t % C::kBufs]);
             mma_commit(&bars[kVFree + (t & 1)]);
             if (n + 1 == n_tiles) mma_commit(&bars[kODone]);
           }
@@ -743,8 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
           m = now;
         }
         if (n > 0 && __any_sync(0xffffffffu, moved)) {
-          // S of this tile was issued before the last P V: O must hold every product so far
-          if (!(ok = (wait_bar(&bars[kPvDone], (uint32_t)((t - 1) & 1), wd)))) break;
+          // S of this tile was issued before the last P V: O must hold every product so far. (One
+          // barrier per score buffer: those kBufs tiles back are done, or S would not be here.)
+          if (!(ok = (wait_bar(&bars[kPvDone + (t - 1) % C::kBufs], (uint32_t)((t - 1) / C::kBufs & 1), wd)))) break;
           tc_fence_after();
           rescale_o<D>(tmem + lane_off + C::kColO, !moved ? 1.f : (before == -INFINITY ? 0.f : ex2_approx(before - now)));
         }

@@ -197,6 +197,25 @@ def test_many_rows_and_far_scales(cuda_lib, fmt, D):
     run(q[:, :, :1].expand(1, 6, 1, D)[:, :2], cache, vals, [n + T - 1], what="one token")
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_references_that_move_at_every_tile(cuda_lib, fmt, D):
+    """Scores that rise by more than a reference holds from tile to tile, for rows of the tiled form:
+    the output is rescaled at every tile, behind every product so far; the same bits every time."""
+    g = torch.Generator().manual_seed(44)
+    n, T = 3000, 33
+    q = torch.randn(1, 4, T, D, generator=g).abs().bfloat16().cuda()
+    k = torch.rand(1, 1, n + T, D, generator=g) * torch.linspace(0.02, 8, n + T)[:, None] * (128 / D)
+    v = torch.randn(1, 1, n + T, D, generator=g)
+    cache = KVCache.allocate(1, 1, n + T, D, fmt)
+    cache_write(cache, k.cuda(), v.cuda(), i32([0]))
+    vals = [t.double().cpu().numpy() for t in cache_read(cache, i32([0]), cache.capacity, dtype=torch.float32)]
+    o, l = run(q, cache, vals, [n], what="rising")
+    for _ in range(20):
+        o2, l2 = tree_attention(q, cache, i32([n]))
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
 def test_window_prefill_then_decode(cuda_lib):
     """A windowed layer's prompt, its rows written to a cache, and its last tokens again as a chain over
     the cache: the rows of the whole prompt's attention."""
