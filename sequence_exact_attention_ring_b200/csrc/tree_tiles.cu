@@ -9,8 +9,8 @@
 // the group's rows is real), the exponentials (128 x 128 per tile at 16 a clock: as long as
 // the products at D = 128) and, with codes, their conversion. What bounds it as built is the
 // chain of one softmax warp (scores ready, maxima, reference, exponentials, P), 4400 clocks a
-// tile, of which two run at a time: 148 CTAs take 51 us for 12 groups of 116 rows and 50k keys
-// of e2m1 (D = 128, 17 us of products), 96 us for 128 full groups and 8k keys of e4m3 (D = 64,
+// tile, of which two run at a time: 148 CTAs take 50 us for 12 groups of 116 rows and 50k keys
+// of e2m1 (D = 128, 17 us of products), 86 us for 128 full groups and 8k keys of e4m3 (D = 64,
 // 21 us). The cache's rows are contiguous and come in as they are, by bulk copies into a ring of
 // raw tiles; eight warps convert them, 8 elements at a time, into the swizzled K and V tiles
 // that the products read. bf16 rows are copied straight into those tiles.
@@ -72,8 +72,8 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxRaw = 4;
 constexpr int kFlags = 16;  // tiles whose form is remembered (more than are ever in flight)
 
-enum Bar { kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kPReady = 8, kQReady = 10, kODone = 11, kDrain = 12,
-           kPair = 13, kMax = 17, kSFull = 25, kPvDone = 28, kRawFull = 31, kRawFree = kRawFull + kMaxRaw,
+enum Bar { kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kPReady = 8, kQReady = 11, kODone = 12, kDrain = 13,
+           kPair = 14, kMax = 18, kSFull = 26, kRawFull = 29, kRawFree = kRawFull + kMaxRaw,
            kRawSeen = kRawFree + kMaxRaw, kNumBars = kRawSeen + 2 * kMaxRaw };
 
 template <int FMT, int D>
@@ -422,7 +422,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
     }
     for (int b = 0; b < 3; ++b) {
       mbar_init(&bars[kSFull + b], 1);
-      mbar_init(&bars[kPvDone + b], 1);
     }
     mbar_init(&bars[kQReady], kSoftmaxWarps);
     mbar_init(&bars[kODone], 1);
@@ -497,7 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
               mma_ts(tmem + C::kColO, tmem + 128 * (t % C::kBufs) + 64 * (k / 4) + 8 * (k % 4), dv + (uint64_t)((k * 16 * 128) >> 4),
                      desc, !(n == 0 && k == 0));
           if (issuer) {
-            mma_commit(&bars[kPvDone + t % C::kBufs]);
             mma_commit(&bars[kVFree + (t & 1)]);
             if (n + 1 == n_tiles) mma_commit(&bars[kODone]);
           }
@@ -744,13 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
           l = m == -INFINITY ? 0.f : l * ex2_approx(m - now);
           m = now;
         }
-        if (n > 0 && __any_sync(0xffffffffu, moved)) {
-          // S of this tile was issued before the last P V: O must hold every product so far. (One
-          // barrier per score buffer: those kBufs tiles back are done, or S would not be here.)
-          if (!(ok = (wait_bar(&bars[kPvDone + (t - 1) % C::kBufs], (uint32_t)((t - 1) / C::kBufs & 1), wd)))) break;
-          tc_fence_after();
-          rescale_o<D>(tmem + lane_off + C::kColO, !moved ? 1.f : (before == -INFINITY ? 0.f : ex2_approx(before - now)));
-        }
+        const float alpha = !moved ? 1.f : (before == -INFINITY ? 0.f : ex2_approx(before - now));
         const float sub = m == -INFINITY ? 0.f : m - C::kLift;
         // (the last columns are still in registers: they go first)
         const bool half = C::kMx && !s_wide[kFlags + t % kFlags];
@@ -760,6 +752,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
           uint32_t pk[32];
           l += exp_pack_as(sr, score_scale, sub, half, pk);
           tmem_st32(tS + c0, pk);  // P of columns c0 .. takes the first half of their place
+        }
+        if (n > 0 && __any_sync(0xffffffffu, moved)) {
+          // O must hold every product so far (V's slot is free when they are done; those three
+          // tiles back are, or S would not be here). The last one waits for the other set's
+          // weights: 3000 clocks where this came before the exponentials.
+          if (!(ok = (wait_bar(&bars[kVFree + ((t - 1) & 1)], (uint32_t)((t - 1) >> 1 & 1), wd)))) break;
+          tc_fence_after();
+          rescale_o<D>(tmem + lane_off + C::kColO, alpha);
         }
         tmem_wait_st();
         tc_fence_before();
