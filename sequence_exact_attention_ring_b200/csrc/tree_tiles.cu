@@ -24,8 +24,8 @@
 // tile, as every step of the chain waited for the one before. Sixteen softmax warps of 64
 // columns, or the reference taken on trust and checked by the sums: within 3 % of this.)
 // Tensor memory: S of three tiles at D = 64, of two at D = 128, then O, Q and its bf16 form;
-// with the third the scores of a set's next tile are there when it ends one (D = 64: 119 ->
-// 107 us). Every role walks the CTA's share of the work by itself (tree_common.cuh), so tiles
+// with the third the scores of a set's next tile are there when it ends one (D = 64: 100 ->
+// 92 us). Every role walks the CTA's share of the work by itself (tree_common.cuh), so tiles
 // of the next unit are filled while the last one is finished.
 //
 // Codes become fp16 operands as in tree_rows.cu, two per conversion instruction, times their
