@@ -459,6 +459,13 @@ int64_t ring_attn_debug_window_visit_counts(int Hq, int Hkv, int64_t S, int D, i
                                             int32_t* counts);
 
 /*
+ * Host only, no GPU. The barriers that the tree kernel for many query rows uses at the t-th
+ * cache tile of a CTA: out[0] the number of score buffers, out[1] of raw-tile slots, out[2..3]
+ * barrier and phase of "scores ready", out[4..5] of "weights ready". out: host int32[6].
+ */
+int ring_attn_debug_tree_barriers(int format, int D, int t, int32_t* out);
+
+/*
  * Device test of the fused kernel's software 2^x (FMA-pipe polynomial used for a
  * fraction of the softmax exponentials): y[i] = 2^x[i] for i < n, n even, device
  * pointers, 16-byte aligned. Relative error <= 1.02e-4 for -126 <= x <= 127;

@@ -83,6 +83,7 @@ SIGNATURES = {
     "ring_attn_window_bwd": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_i64,
                                       _c_int, _c_i64, _c_i64, _c_float, _vp, _c_size, _vp]),
     "ring_attn_debug_window_visit_counts": (_c_i64, [_c_int, _c_int, _c_i64, _c_int, _c_i64, _c_i64, _c_int, _vp]),
+    "ring_attn_debug_tree_barriers": (_c_int, [_c_int, _c_int, _c_int, ctypes.POINTER(ctypes.c_int32)]),
     "ring_attn_debug_bwd_visit_counts": (_c_i64, [_c_i64, _c_int, _c_int, _c_int, _c_int, _vp]),
     "ring_attn_fwd_noalloc": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_i64, _c_int, _c_int,
                                        _c_int, _c_int, _c_float, _c_int, _vp, ctypes.POINTER(_vp)]),
@@ -263,6 +264,13 @@ def ring_attn_window_bwd(q, k, v, out, lse, dout, dq, dk, dv, B, Hq, Hkv, S, D, 
 
 def ring_attn_debug_window_visit_counts(Hq, Hkv, S, D, window, sinks, pass_, counts) -> int:
     return load().ring_attn_debug_window_visit_counts(Hq, Hkv, S, D, window, sinks, pass_, counts)
+
+
+def ring_attn_debug_tree_barriers(format_, D, t):
+    """(score buffers, raw slots, scores' barrier, its phase, weights' barrier, its phase) at tile t."""
+    out = (ctypes.c_int32 * 6)()
+    check(load().ring_attn_debug_tree_barriers(format_, D, t, out), "ring_attn_debug_tree_barriers")
+    return tuple(out)
 
 
 def ring_attn_debug_bwd_visit_counts(S, P, causal, layout, pass_, counts) -> int:

@@ -689,6 +689,14 @@ int64_t ring_attn_debug_window_visit_counts(int Hq, int Hkv, int64_t S, int D, i
   return pass == 0 ? window_fwd_visits(g, counts) : window_bwd_visits(g, pass - 1, counts);
 }
 
+int ring_attn_debug_tree_barriers(int format, int D, int t, int32_t* out) {
+  if (format != RING_ATTN_CACHE_BF16 && format != RING_ATTN_CACHE_MXFP8 && format != RING_ATTN_CACHE_MXFP4)
+    return RING_ATTN_EINVAL;
+  if (D != 64 && D != 128) return RING_ATTN_EUNSUPPORTED;
+  if (t < 0 || !out) return RING_ATTN_EINVAL;
+  return tree_tile_barriers(format, D, t, out);
+}
+
 int ring_attn_debug_exp2(const float* x, float* y, int64_t n, void* stream) {
   if (!x || !y || n < 0 || (n & 1)) return RING_ATTN_EINVAL;
   if (!aligned16(x) || !aligned16(y)) return RING_ATTN_EALIGN;

@@ -127,6 +127,9 @@ int launch_tree(const CacheView& c, const void* q, const int64_t* qs, void* out,
                 const int32_t* parents, const int32_t* counts, int Hq, int T, int window, int sinks, float scale,
                 void* workspace, uint64_t watchdog_ns, cudaStream_t stream);
 
+// The barriers of its form for many rows at tile t (see ring_attn_debug_tree_barriers).
+int tree_tile_barriers(int format, int D, int t, int32_t* out);
+
 // Causal attention with a sliding window and sinks (bf16): forward, and gradients with
 // `scratch` of window_bwd_scratch_bytes(g).
 int launch_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse, const WinGeom& g,

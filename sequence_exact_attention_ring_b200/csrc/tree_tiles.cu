@@ -76,6 +76,13 @@ enum Bar { kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kPReady = 8, kQReady 
            kPair = 14, kMax = 18, kSFull = 26, kRawFull = 29, kRawFree = kRawFull + kMaxRaw,
            kRawSeen = kRawFree + kMaxRaw, kNumBars = kRawSeen + 2 * kMaxRaw };
 
+// Which of a kind's barriers tile t uses, and the phase of it that the tile completes.
+struct Turn {
+  int at;
+  uint32_t phase;
+};
+RA_HD Turn turn(int t, int n) { return {t % n, (uint32_t)(t / n & 1)}; }
+
 template <int FMT, int D>
 struct Cfg {
   static constexpr bool kMx = FMT != RING_ATTN_CACHE_BF16;
@@ -84,6 +91,14 @@ struct Cfg {
   static constexpr int kBufs = D == 64 ? 3 : 2;
   static constexpr uint32_t kColO = 128 * kBufs, kColQ = kColO + D, kColQb = kColQ + D / 2;
   static_assert(kColQb + D / 2 <= kTmemCols, "tensor memory");
+  // "Scores of tile t are there" and "its weights are": a barrier each per score buffer. Scores of
+  // tile t + kBufs are asked for only once the weights of tile t were waited for, so no barrier
+  // completes a second phase before the first was seen. (With two for the weights of three
+  // buffers a set of softmax warps could finish tiles t and t + 2 while the products still
+  // waited for V of tile t, and these then waited for a phase that nothing completes.)
+  static RA_HD Turn s_full(int t) { return turn(t, kBufs); }
+  static RA_HD Turn p_ready(int t) { return turn(t, kBufs); }
+  static_assert(kPReady + kBufs <= kQReady && kSFull + kBufs <= kRawFull, "barriers per score buffer");
   static constexpr int kChunks = kRowBytes / 16;       // per row
   static constexpr int kTileChunks = TK * kChunks;     // 16-byte chunks of a tile of bf16 rows
   static constexpr int kTileBytes = TK * D * 2;        // a bf16 tile
@@ -418,10 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
       mbar_init(&bars[kVFull + b], kFillWarps);
       mbar_init(&bars[kKFree + b], 1);
       mbar_init(&bars[kVFree + b], 1);
-      mbar_init(&bars[kPReady + b], kSoftmaxWarps / 2);
     }
-    for (int b = 0; b < 3; ++b) {
+    for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(&bars[kSFull + b], 1);
+      mbar_init(&bars[kPReady + b], kSoftmaxWarps / 2);
     }
     mbar_init(&bars[kQReady], kSoftmaxWarps);
     mbar_init(&bars[kODone], 1);
@@ -474,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
             if (issuer)
               mma_ts(tmem + 128 * (t % C::kBufs), qa + 8 * k, dk + (uint64_t)(((k / 4) * kBoxBytes + (k % 4) * 32) >> 4), desc, k > 0);
           if (issuer) {
-            mma_commit(&bars[kSFull + t % C::kBufs]);
+            mma_commit(&bars[kSFull + C::s_full(t).at]);
             mma_commit(&bars[kKFree + (t & 1)]);
           }
           return true;
@@ -486,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
         for (int n = 0; ok && n < n_tiles; ++n) {
           const int t = t0 + n;
           if (!(ok = (wait_bar(&bars[kVFull + (t & 1)], (uint32_t)(t >> 1 & 1), wd)))) break;
-          if (!(ok = (wait_bar(&bars[kPReady + (t & 1)], (uint32_t)(t >> 1 & 1), wd)))) break;
+          if (!(ok = (wait_bar(&bars[kPReady + C::p_ready(t).at], C::p_ready(t).phase, wd)))) break;
           tc_fence_after();
           const uint64_t dv = smem_desc_sw128(sbase + C::kOffV + (t & 1) * C::kTileBytes, kBoxBytes, 1024);
           const uint32_t desc = C::kMx && !s_wide[kFlags + t % kFlags] ? C::kIdescO & ~C::kBf16Types : C::kIdescO;
@@ -692,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
         // every row sees the whole tile
         const bool whole = kb + TK <= ks.n &&
                            (p.window <= 0 || kb + TK <= p.sinks || kb >= ks.n + p.T - p.window);
-        if (!(ok = (wait_bar(&bars[kSFull + t % C::kBufs], (uint32_t)(t / C::kBufs & 1), wd)))) break;
+        if (!(ok = (wait_bar(&bars[kSFull + C::s_full(t).at], C::s_full(t).phase, wd)))) break;
         tc_fence_after();
         const uint32_t tS = tmem + lane_off + 128 * (t % C::kBufs);
         if (__builtin_expect(!whole, 0)) {
@@ -764,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kPReady + hh]);
+        if (lane == 0) mbar_arrive(&bars[kPReady + C::p_ready(t).at]);
       }
       if (!ok) break;
       // the two warps of the rows join their sums (m never falls: the larger one is the row's)
@@ -848,6 +863,15 @@ int launch(const Params& p, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ECUDA;
 }
 
+template <int FMT, int D>
+int barriers(int t, int32_t* out) {
+  using C = Cfg<FMT, D>;
+  const int32_t x[6] = {C::kBufs, C::kRaw, C::s_full(t).at, (int32_t)C::s_full(t).phase,
+                        C::p_ready(t).at, (int32_t)C::p_ready(t).phase};
+  for (int i = 0; i < 6; ++i) out[i] = x[i];
+  return RING_ATTN_OK;
+}
+
 template <int FMT>
 int launch_d(const Params& p, cudaStream_t stream) {
   return p.c.D == 64 ? launch<FMT, 64>(p, stream) : launch<FMT, 128>(p, stream);
@@ -864,4 +888,14 @@ int launch_tiles(const Params& p, cudaStream_t stream) {
 }
 
 }  // namespace tree
+
+int tree_tile_barriers(int format, int D, int t, int32_t* out) {
+  using namespace tree::tiles;
+  switch (format) {
+    case RING_ATTN_CACHE_BF16: return D == 64 ? barriers<RING_ATTN_CACHE_BF16, 64>(t, out) : barriers<RING_ATTN_CACHE_BF16, 128>(t, out);
+    case RING_ATTN_CACHE_MXFP8: return D == 64 ? barriers<RING_ATTN_CACHE_MXFP8, 64>(t, out) : barriers<RING_ATTN_CACHE_MXFP8, 128>(t, out);
+    default: return D == 64 ? barriers<RING_ATTN_CACHE_MXFP4, 64>(t, out) : barriers<RING_ATTN_CACHE_MXFP4, 128>(t, out);
+  }
+}
+
 }  // namespace ringattn
