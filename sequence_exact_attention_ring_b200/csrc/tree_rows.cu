@@ -727,7 +727,9 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
     }
     cp_wait<0>();
 
-    // join the four warps' states: weights 2^(m_w - M), and 2^E_w on what carries it, then O / l
+    // Join the four warps' states: weights 2^(m_w - M), and 2^E_w on what carries it, then O / l.
+    // A state that saw no key is known by its sum, which is 0: scores that are NaN leave the
+    // reference at -inf too (no maximum takes them up), but make the sum NaN, and with it the row.
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -772,16 +774,16 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
         for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float mw = s_ml[w][r][0];
-          if (mw == -INFINITY) continue;
-          const float a = ex2_approx(mw - M);
-          L += a * s_ml[w][r][1];
+          const float lw = s_ml[w][r][1];
+          if (lw == 0.f) continue;
+          const float a = ex2_approx(s_ml[w][r][0] - M);
+          L += a * lw;
           const float av = a * exp2f(s_ml[w][r][2] - E);
           const float* src = so + (w * kRows + r) * (D + 4) + d0;
 #pragma unroll
           for (int e = 0; e < kPer; ++e) acc[e] = fmaf(av, src[e], acc[e]);
         }
-        const bool none = M == -INFINITY;
+        const bool none = L == 0.f;
         const float inv = none ? 0.f : 1.f / L;
         const float up = exp2f(E);  // applied apart from 1 / L: the two together may leave fp32's range
 #pragma unroll
@@ -871,19 +873,18 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = M;
   __syncthreads();
   M = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+  if (M == -INFINITY) M = 0.f;  // no part is finite: a NaN among them still reaches the sum
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  if (M != -INFINITY) {
 #pragma unroll 4
-    for (int i = part; i < parts; i += kPar) {
-      const float w = ex2_approx(lse[i * p.rows_per_group] - M);
-      const float4 v = *reinterpret_cast<const float4*>(src + i * stride);
-      sum += w;  // an empty part's row is 0 and so is its weight
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
-    }
+  for (int i = part; i < parts; i += kPar) {
+    const float w = ex2_approx(lse[i * p.rows_per_group] - M);
+    const float4 v = *reinterpret_cast<const float4*>(src + i * stride);
+    sum += w;  // an empty part's row is 0 and so is its weight
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
   }
   s_acc[part][d4] = acc;
   if (d4 == 0) s_sum[part] = sum;
@@ -899,10 +900,10 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
     a.z += s_acc[i][d4].z;
     a.w += s_acc[i][d4].w;
   }
-  const float inv = M == -INFINITY ? 0.f : 1.f / tot;
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;
   reinterpret_cast<uint2*>(p.out + orow * D)[d4] =
       make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-  if (d4 == 0) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(tot)) * 0.69314718055994530942f;
+  if (d4 == 0) p.lse[orow] = (M + log2f(tot)) * 0.69314718055994530942f;  // (log2 0 = -inf)
 }
 
 // The same for units of many rows, whose parts are fewer. The unit's parts are found once for
@@ -946,23 +947,22 @@ __global__ void __launch_bounds__(128) tree_merge_rows_kernel(const __grid_const
   for (int i = sub + 8 * grp; i < parts; i += 8 * G) M = fmaxf(M, lse[(int64_t)i * p.rows_per_group]);
 #pragma unroll
   for (int o = 4 * G; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(row_lanes, M, o));
+  if (M == -INFINITY) M = 0.f;  // as above
   float sum = 0.f;
   float4 acc[kVec];
 #pragma unroll
   for (int e = 0; e < kVec; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (M != -INFINITY) {
 #pragma unroll 4
-    for (int i = grp; i < parts; i += G) {
-      const float w = ex2_approx(lse[(int64_t)i * p.rows_per_group] - M);
-      sum += w;
+  for (int i = grp; i < parts; i += G) {
+    const float w = ex2_approx(lse[(int64_t)i * p.rows_per_group] - M);
+    sum += w;
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {  // an empty part's row is 0 and so is its weight
-        const float4 v = *reinterpret_cast<const float4*>(src + i * stride + 32 * e);
-        acc[e].x = fmaf(w, v.x, acc[e].x);
-        acc[e].y = fmaf(w, v.y, acc[e].y);
-        acc[e].z = fmaf(w, v.z, acc[e].z);
-        acc[e].w = fmaf(w, v.w, acc[e].w);
-      }
+    for (int e = 0; e < kVec; ++e) {  // an empty part's row is 0 and so is its weight
+      const float4 v = *reinterpret_cast<const float4*>(src + i * stride + 32 * e);
+      acc[e].x = fmaf(w, v.x, acc[e].x);
+      acc[e].y = fmaf(w, v.y, acc[e].y);
+      acc[e].z = fmaf(w, v.z, acc[e].z);
+      acc[e].w = fmaf(w, v.w, acc[e].w);
     }
   }
 #pragma unroll
@@ -977,12 +977,12 @@ __global__ void __launch_bounds__(128) tree_merge_rows_kernel(const __grid_const
     }
   }
   if (grp != 0) return;
-  const float inv = M == -INFINITY ? 0.f : 1.f / sum;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int e = 0; e < kVec; ++e)
     *reinterpret_cast<uint2*>(dst + 32 * e) =
         make_uint2(pack_bf16x2(acc[e].x * inv, acc[e].y * inv), pack_bf16x2(acc[e].z * inv, acc[e].w * inv));
-  if (sub == 0) p.lse[orow] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * 0.69314718055994530942f;
+  if (sub == 0) p.lse[orow] = (M + log2f(sum)) * 0.69314718055994530942f;
 }
 
 template <int FMT, int D, int NT>

@@ -754,7 +754,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kMax + 2 * wq + hh]);
         if (m != now) {
-          l = m == -INFINITY ? 0.f : l * ex2_approx(m - now);
+          // (before the first finite score l is 0, or NaN, which the row keeps)
+          if (m != -INFINITY) l *= ex2_approx(m - now);
           m = now;
         }
         const float alpha = !moved ? 1.f : (before == -INFINITY ? 0.f : ex2_approx(before - now));
@@ -790,14 +791,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tiles_kernel(const __grid_co
       if (!(ok = (wait_bar(&bars[kPair + wq], 1, wd)))) break;
       const float m_other = s_m[(hh ^ 1) * 128 + r], l_other = s_x[(hh ^ 1) * 128 + r];
       const float m_row = fmaxf(m, m_other);
-      l = m == -INFINITY ? 0.f : l * ex2_approx(m - m_row);
-      const float lo2 = m_other == -INFINITY ? 0.f : l_other * ex2_approx(m_other - m_row);
+      if (m != -INFINITY) l *= ex2_approx(m - m_row);
+      const float lo2 = m_other == -INFINITY ? l_other : l_other * ex2_approx(m_other - m_row);
       m = m_row;
       if (!(ok = (wait_bar(&bars[kODone], (uint32_t)(parts & 1), wd)))) break;
       tc_fence_after();
       // l carries the same 2^kLift as O
       const float L = hh == 0 ? l + lo2 : lo2 + l;  // the same sum in both
-      const bool none = m == -INFINITY;
+      const bool none = L == 0.f;  // a row of keys that are not finite has L = NaN and m = -inf
       const float inv = none ? 0.f : pow2i(-C::kBias) / L;  // O carries V's factor as well
       const float lse2 = none ? -INFINITY : m + log2f(L * (C::kMx ? 0x1p-9f : 1.f));
       const int64_t slot = (int64_t)blockIdx.x + part.unit;
