@@ -323,8 +323,11 @@ int ring_attn_cache_read(const void* k_cache, const void* v_cache, const void* k
  * capacity make that sequence's rows 0 and -inf, and a parent outside [-1, j) counts as -1;
  * both are reported as RING_ATTN_EINVAL by ring_attn_status. Rows that no node can see
  * (behind the last node, or below the window) are not read and may hold anything; every
- * other row must be finite (a block that is not finite makes the rows that see it NaN), and
- * below 2^90 in magnitude.
+ * other row must be finite, and below 2^90 in magnitude, and so must q. Where one is not: a
+ * query row with a NaN, or one that sees a row of K with a NaN (or a block marked 255), gets
+ * out and lse NaN; a row of V with one makes out NaN in the dimensions that hold it (in the
+ * block), for the query rows that see it and perhaps for others of its sequence and kv head.
+ * The remaining rows and dimensions are as without it.
  * Results do not depend on timing: the same call gives the same bits.
  */
 size_t ring_attn_tree_workspace_bytes(int format, int B, int Hq, int Hkv, int64_t capacity, int D, int T);

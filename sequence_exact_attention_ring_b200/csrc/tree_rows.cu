@@ -350,10 +350,13 @@ struct Warp {
   }
 
   // The largest and smallest scale bytes of the step's live K rows (ref[0], low[0]) and V rows
-  // (ref[1], low[1]). Dead rows hold zero codes under scale bytes that may be anything: theirs
-  // become the reference, so that no factor is out of range.
-  static __device__ __forceinline__ void scale_range(uint8_t* st, bool all_live, uint32_t live_rows, int (&ref)[2],
+  // (ref[1], low[1]); false if one of them is 255. Such a block, which is not finite, is no part
+  // of the reference: under 2^127 the step's other blocks, which rows that do not see that one
+  // still need, would lose their bits. Dead rows hold zero codes under scale bytes that may be
+  // anything: theirs become the reference, so that no factor is out of range.
+  static __device__ __forceinline__ bool scale_range(uint8_t* st, bool all_live, uint32_t live_rows, int (&ref)[2],
                                                      int (&low)[2]) {
+    bool finite = true;
     using Word = typename std::conditional<F::kScaleRow == 4, uint32_t, uint16_t>::type;
     const int lane = threadIdx.x % 32;
     const bool mine = all_live || (live_rows >> lane & 1);
@@ -373,11 +376,20 @@ struct Warp {
       }
       ref[i] = (int)__reduce_max_sync(0xffffffffu, mine ? hi : 0u);
       low[i] = (int)__reduce_min_sync(0xffffffffu, mine ? lo : 255u);
+      if (__builtin_expect(ref[i] == 255, 0)) {
+        finite = false;
+        hi = 0;
+#pragma unroll 1
+        for (uint32_t x = w; x != 0; x >>= 8)
+          if ((x & 255u) != 255u) hi = max(hi, x & 255u);
+        ref[i] = (int)__reduce_max_sync(0xffffffffu, mine ? hi : 0u);
+      }
       if (!all_live) {
-        if (!mine) *sc = (Word)(min(ref[i], 254) * 0x01010101u);
+        if (!mine) *sc = (Word)(ref[i] * 0x01010101u);
         __syncwarp();
       }
     }
+    return finite;
   }
 
   // d += a b with the query fragment in fp16 and a in fp16 or bf16.
@@ -634,10 +646,8 @@ __global__ void __launch_bounds__(kThreads, Fmt<FMT, D>::per_sm(NT)) tree_rows_k
         if (F::kMx) {
           if (!whole) live = __ballot_sync(0xffffffffu, key_live(p, ks, kb + lane));
           int low[2];
-          W::scale_range(st, whole, live, ref, low);
-          half = ref[0] < 255 && ref[1] < 255 && ref[0] - low[0] <= kSpread && ref[1] - low[1] <= kSpread;
-          ref[0] = min(ref[0], 254);
-          ref[1] = min(ref[1], 254);
+          half = W::scale_range(st, whole, live, ref, low);
+          half = half && ref[0] - low[0] <= kSpread && ref[1] - low[1] <= kSpread;
           if (ref[1] > v_ref) {  // raise E: O carries 2^-E
             const float a = pow2(v_ref - ref[1]);
 #pragma unroll

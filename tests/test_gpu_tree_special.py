@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import oracle
-from sequence_exact_attention_ring_b200 import cache_write, status, tree_attention, tree_workspace
+from sequence_exact_attention_ring_b200 import cache_read, cache_write, status, tree_attention, tree_workspace
 from test_gpu_tree import FORMATS, check, i32, make, weight_floor
 
 pytestmark = pytest.mark.gpu
@@ -108,3 +108,59 @@ def test_all_keys_not_finite(cuda_lib, fmt, D):
                 poison(cache, 0, 0, row, "k", block=row % 2)
             out, lse = attend(q, cache, [n])
             assert torch.isnan(out).all() and torch.isnan(lse).all(), (T, rep, n)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("exp", [0, -24])
+def test_key_that_only_some_nodes_see(cuda_lib, fmt, D, exp):
+    """A drafted node's key is not finite: it and its descendants come out NaN, the other branch of the tree
+    exactly as well as ever (also where its keys and values are small against any fixed reference)."""
+    parents = {3: [-1, -1, 1], 4: [-1, 0, -1, 2], 20: [*range(-1, 9), -1, *range(10, 19)]}
+    for T, rep, n in ((3, 1, 29), (4, 4, 100), (20, 4, 300), (20, 4, 0)):
+        par = parents[T]
+        assert all(-1 <= x < i for i, x in enumerate(par))
+        q, cache, _ = make(1, rep, 1, D, T, [n], fmt, 305)
+        g = torch.Generator().manual_seed(306)
+        new = torch.randn(2, 1, 1, n + T, D, generator=g)
+        cache_write(cache, (new[0] * 2.0 ** exp).bfloat16().cuda(), (new[1] * 2.0 ** exp).bfloat16().cuda(), i32([0]))
+        q = (q.float() * 2.0 ** -exp).bfloat16()
+        poison(cache, 0, 0, n, "k")
+        out, lse = attend(q, cache, [n], [par])
+        vals = [t.double().cpu().numpy() for t in cache_read(cache, i32([0]), cache.capacity, dtype=torch.float32)]
+        ref = oracle.tree_reference(q.double().cpu().numpy(), *vals, [n], [par], None, 0, 0, D ** -0.5)
+        below = np.zeros(T, dtype=bool)
+        for i in range(T):
+            below[i] = i == 0 or (par[i] >= 0 and below[par[i]])
+        assert below.any() and not below.all()
+        bad = torch.from_numpy(below).cuda()
+        assert torch.isnan(out[0][:, bad]).all() and torch.isnan(lse[0][:, bad]).all()
+        keep = torch.zeros_like(lse, dtype=torch.bool)
+        keep[:, :, ~bad] = True
+        keep_np = keep.cpu().numpy()
+        check(out[keep], lse[keep], tuple(x[keep_np] for x in ref), D, f"{T} {n}", weight_floor(cache, vals, [n], T))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("exp", [0, -24])
+def test_value_block_that_is_not_finite(cuda_lib, fmt, D, exp):
+    """A block of one committed row of V is not finite: out is NaN in the dimensions that it holds, and what
+    it would be without it in the others; lse has nothing to do with V."""
+    for T, rep, n in ((1, 4, 200), (3, 4, 700), (20, 4, 700)):
+        q, cache, _ = make(1, rep, 1, D, T, [n], fmt, 307)
+        g = torch.Generator().manual_seed(308)
+        v = (torch.randn(1, 1, n + T, D, generator=g) * 2.0 ** exp).bfloat16().cuda()
+        cache_write(cache, torch.randn(1, 1, n + T, D, generator=g).bfloat16().cuda(), v, i32([0]))
+        poison(cache, 0, 0, 37, "v")
+        out, lse = attend(q, cache, [n])
+        vals = [t.double().cpu().numpy() for t in cache_read(cache, i32([0]), cache.capacity, dtype=torch.float32)]
+        hit = np.isnan(vals[1][0, 0, 37])
+        assert hit[32:64].any() and not hit[:32].any()
+        assert torch.isnan(out[..., torch.from_numpy(hit).cuda()]).all()
+        vals[1][0, 0, 37, hit] = 0.0
+        ref = oracle.tree_reference(q.double().cpu().numpy(), *vals, [n], None, None, 0, 0, D ** -0.5)
+        O, L, A, E = ref
+        keep = ~hit
+        check(out[..., torch.from_numpy(keep).cuda()], lse, (O[..., keep], L, A[..., keep], E), D, f"{T}",
+              weight_floor(cache, vals, [n], T))
