@@ -307,6 +307,22 @@ def _scratch(workspace, need, device, stream=None):
     return workspace
 
 
+def _share(stream, device, inputs, outputs=()):
+    """For a call issued on a `stream` other than the current one: torch's allocator hands memory out again
+    as soon as its own stream allows, so it is told that `stream` uses the inputs, and that the outputs will
+    be used on the current stream too. (Ordering the two streams stays the caller's.)"""
+    if stream is None:
+        return
+    current = torch.cuda.current_stream(device)
+    if current.cuda_stream == stream.cuda_stream:
+        return
+    for t in (*inputs, *outputs):
+        if t is not None:
+            t.record_stream(stream)
+    for t in outputs:
+        t.record_stream(current)
+
+
 def window_attention(q, k, v, window: int, sinks: int = 0, scale: float | None = None, out=None, lse=None,
                      workspace=None, stream=None):
     """Causal attention in which token t sees the last `window` tokens up to itself and the
@@ -325,6 +341,7 @@ def window_attention(q, k, v, window: int, sinks: int = 0, scale: float | None =
                   lse.data_ptr(), B, Hq, k.shape[1], S, D, min(int(window), S), min(int(sinks), S), scale, workspace.data_ptr(),
                   workspace.nbytes, _stream_on(stream, dev))
     _b.check(rc, "ring_attn_window_fwd")
+    _share(stream, dev, (q, k, v, workspace), (out, lse))
     return out, lse
 
 
@@ -355,6 +372,7 @@ def window_attention_backward(q, k, v, out, lse, dout, window: int, sinks: int =
                   lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, k.shape[1], S, D,
                   min(int(window), S), min(int(sinks), S), scale, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
     _b.check(rc, "ring_attn_window_bwd")
+    _share(stream, dev, (q, k, v, out, lse, dout, workspace), (dq, dk, dv))
     return dq, dk, dv
 
 

@@ -10,7 +10,7 @@ import math
 import torch
 
 from . import binding as _b
-from .api import _DTYPES, _call_on, _like, _scratch, _stream_on
+from .api import _DTYPES, _call_on, _like, _scratch, _share, _stream_on
 
 _FORMATS = {"bf16": _b.CACHE_BF16, "mxfp8": _b.CACHE_MXFP8, "mxfp4": _b.CACHE_MXFP4}
 _BLOCK = 32
@@ -68,7 +68,10 @@ class KVCache:
         return cls(format, *rows, *scales)
 
     def bytes(self) -> int:
-        return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scale, self.v_scale) if t is not None)
+        return sum(t.numel() * t.element_size() for t in self._tensors() if t is not None)
+
+    def _tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
 
     def _pointers(self):
         if self.k_scale is None:
@@ -142,6 +145,7 @@ def cache_write(cache: KVCache, k_new, v_new, start, count=None, index=None, wor
                   _FORMATS[cache.format], cache.B, cache.Hkv, cache.capacity, cache.D, T, T_src, p_start, p_count,
                   p_index, ws, ws_bytes, _stream_on(stream, dev))
     _b.check(rc, "ring_attn_cache_write")
+    _share(stream, dev, (*cache._tensors(), k_new, v_new, start, count, index, workspace))
 
 
 def cache_read(cache: KVCache, start, T: int, count=None, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
@@ -164,6 +168,7 @@ def cache_read(cache: KVCache, start, T: int, count=None, dtype=torch.bfloat16, 
                   cache.capacity, cache.D, T, p_start, p_count, k_out.data_ptr(), v_out.data_ptr(), _DTYPES[dtype],
                   _stream_on(stream, dev))
     _b.check(rc, "ring_attn_cache_read")
+    _share(stream, dev, (*cache._tensors(), start, count), (k_out, v_out))
     return k_out, v_out
 
 
@@ -210,4 +215,5 @@ def tree_attention(q, cache: KVCache, lengths, parents=None, counts=None, window
                   out.data_ptr(), lse.data_ptr(), B, Hq, cache.Hkv, cache.capacity, D, T, p_len, p_par, p_cnt,
                   _int31(window), _int31(sinks), scale, workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
     _b.check(rc, "ring_attn_tree")
+    _share(stream, dev, (*cache._tensors(), q, lengths, parents, counts, workspace), (out, lse))
     return out, lse
