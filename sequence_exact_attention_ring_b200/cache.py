@@ -120,7 +120,8 @@ def cache_write(cache: KVCache, k_new, v_new, start, count=None, index=None, wor
     Cache row start[b] + i becomes new row i for i < count[b] (default: all T). With
     index [B, n] int32 there are n rows to write and row i comes from new row index[b, i].
     No other row is touched; rows that would fall outside the cache are skipped, which
-    `status` reports for a given `workspace` (uint8, >= 256 bytes). Asynchronous on `stream`.
+    `status` reports for a given `workspace` (uint8, >= 256 bytes). The new rows must not be
+    rows of the cache itself. Asynchronous on `stream`.
     """
     dev = _on_device(cache)
     for t in (k_new, v_new):
@@ -134,12 +135,19 @@ def cache_write(cache: KVCache, k_new, v_new, start, count=None, index=None, wor
         raise ValueError("k_new and v_new must have one shape")
     T_src = k_new.shape[2]
     T = T_src if index is None else index.shape[-1]
-    if T == 0 or T_src == 0:
-        return
     p_start = _int_rows(_required(start, "start"), (cache.B,), "start", dev)
     p_count = _int_rows(count, (cache.B,), "count", dev)
     p_index = _int_rows(index, (cache.B, T), "index", dev)
     ws, ws_bytes = (0, 0) if workspace is None else (_scratch(workspace, 0, dev).data_ptr(), workspace.nbytes)
+    if T == 0:  # nothing to write, which the status word has to say
+        if workspace is not None:
+            if ws_bytes < 256:
+                raise _b.RingAttnError(_b.EWORKSPACE, "ring_attn_cache_write")
+            with torch.cuda.stream(stream):
+                workspace.reshape(-1).view(torch.uint8)[:4].zero_()
+        return
+    if T_src == 0:
+        raise ValueError("index picks rows of k_new and v_new, which have none")
     rc = _call_on(dev, _b.ring_attn_cache_write, k_new.data_ptr(), v_new.data_ptr(),
                   (*_strides(k_new), *_strides(v_new)), _DTYPES[k_new.dtype], *cache._pointers(),
                   _FORMATS[cache.format], cache.B, cache.Hkv, cache.capacity, cache.D, T, T_src, p_start, p_count,
