@@ -1,9 +1,14 @@
-"""GPU: calls of the cache and of attention over it that the other files do not make: writes of no rows."""
+"""GPU: calls of the cache and of attention over it that the other files do not make: writes of no rows,
+batches of more than a warp of sequences, blocks of zeros.
+
+Tolerances are test_gpu_tree.py's.
+"""
+import numpy as np
 import pytest
 import torch
 
 from sequence_exact_attention_ring_b200 import (KVCache, RingAttnError, binding, cache_read, cache_write, status)
-from test_gpu_tree import i32
+from test_gpu_tree import FORMATS, i32, make, random_tree, run
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +45,46 @@ def test_write_of_no_rows_clears_the_status(cuda_lib):
         cache_write(cache, none, none, start, index=i32([[0], [0]]))
     k, v = cache_read(cache, start, 0)
     assert k.shape == v.shape == (2, 1, 0, 64)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("B", [33, 70])
+@pytest.mark.parametrize("T,rep", [(1, 2), (3, 8)])
+def test_more_sequences_than_a_warp_has_lanes(cuda_lib, fmt, B, T, rep):
+    """Lengths from 0 to some hundreds, empty and refused sequences among them: their shares are found 32
+    sequences at a time."""
+    r = np.random.default_rng(B)
+    lengths = [int(x) for x in r.integers(0, 700, B)]
+    lengths[0] = lengths[31] = 0
+    lengths[32], lengths[-1] = 699, 1
+    q, cache, vals = make(B, rep, 1, 64, T, lengths, fmt, 401)
+    counts = [int(x) for x in r.integers(0, T + 1, B)]
+    counts[32] = T
+    run(q, cache, vals, lengths, random_tree(B, T, 402), counts, what="counts")
+    run(q, cache, vals, lengths, what="chain")
+    run(q, cache, vals, lengths, window=65, sinks=3, what="window")
+
+
+def test_more_sequences_than_ctas(cuda_lib):
+    """More units than CTAs: most of them are done by one CTA each."""
+    B, T = 200, 2
+    lengths = [(37 * b) % 90 for b in range(B)]
+    for rep in (2, 12):
+        q, cache, vals = make(B, 2 * rep, 2, 64, T, lengths, "mxfp8", 403)
+        run(q, cache, vals, lengths, what=f"{rep}")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_rows_of_zeros_among_others(cuda_lib, fmt):
+    """Blocks of zeros (scale byte 0) in K and in V, as padded head dimensions leave them, for both forms."""
+    n, D = 400, 128
+    g = torch.Generator().manual_seed(404)
+    for T, rep in ((1, 4), (20, 4)):
+        cache = KVCache.allocate(1, 1, n + T, D, fmt)
+        k, v = torch.randn(1, 1, n + T, D, generator=g), torch.randn(1, 1, n + T, D, generator=g)
+        k[..., 96:], v[..., 96:] = 0.0, 0.0
+        cache_write(cache, k.cuda(), v.cuda(), i32([0]))
+        vals = [t.double().cpu().numpy() for t in cache_read(cache, i32([0]), cache.capacity, dtype=torch.float32)]
+        q = torch.randn(1, rep, T, D, generator=g).bfloat16().cuda()
+        out, _ = run(q, cache, vals, [n], what="padded")
+        assert not out[..., 96:].any()
