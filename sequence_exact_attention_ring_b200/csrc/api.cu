@@ -434,7 +434,7 @@ size_t ring_attn_tree_workspace_bytes(int format, int B, int Hq, int Hkv, int64_
   CacheView c;
   const void* some = reinterpret_cast<const void*>(uintptr_t(256));  // only the sizes are looked at
   if (check_cache(some, some, some, some, format, B, Hkv, capacity, D, &c) != RING_ATTN_OK) return 0;
-  if (Hq <= 0 || Hq % Hkv != 0 || T < 1 || T > 64 || (int64_t)B * Hq > (1 << 24)) return 0;
+  if (Hq <= 0 || Hq % Hkv != 0 || T < 1 || T > kTreeMaxNodes || (int64_t)B * Hq > (1 << 24)) return 0;
   return tree_workspace_bytes(c, Hq, T);
 }
 
@@ -446,7 +446,7 @@ int ring_attn_tree(const void* q, const int64_t* q_strides, const void* k_cache,
   CacheView c;
   int rc = check_cache(k_cache, v_cache, k_scale, v_scale, format, B, Hkv, capacity, D, &c);
   if (rc) return rc;
-  if (Hq <= 0 || Hq % Hkv != 0 || T < 1 || T > 64 || (int64_t)B * Hq > (1 << 24)) return RING_ATTN_EINVAL;
+  if (Hq <= 0 || Hq % Hkv != 0 || T < 1 || T > kTreeMaxNodes || (int64_t)B * Hq > (1 << 24)) return RING_ATTN_EINVAL;
   if (!q || !q_strides || !out || !lse || !lengths || window < 0 || sinks < 0) return RING_ATTN_EINVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned4(lse) || !aligned4(lengths) || !aligned4(parents) ||
       !aligned4(counts) || !strides_aligned(q_strides, 3, 2))

@@ -121,7 +121,8 @@ int launch_cache_write(const CacheView& c, const void* k_new, const void* v_new,
 int launch_cache_read(const CacheView& c, int T, const int32_t* start, const int32_t* count, void* k_out, void* v_out,
                       int dtype, cudaStream_t stream);
 
-// Attention of up to 64 drafted tokens per sequence over a cache.
+// Attention of up to kTreeMaxNodes drafted tokens per sequence over a cache.
+constexpr int kTreeMaxNodes = 64;
 size_t tree_workspace_bytes(const CacheView& c, int Hq, int T);
 int launch_tree(const CacheView& c, const void* q, const int64_t* qs, void* out, float* lse, const int32_t* lengths,
                 const int32_t* parents, const int32_t* counts, int Hq, int T, int window, int sinks, float scale,

@@ -32,8 +32,6 @@
 namespace ringattn {
 namespace tree {
 
-constexpr int kMaxNodes = 64;
-
 // Functions that run once per unit: calls, except in kernels that move registers between
 // warpgroups (setmaxnreg), which cannot call functions.
 #ifdef TREE_INLINE
@@ -184,6 +182,7 @@ __device__ __forceinline__ int warp_find_sequence(const Params& p, uint32_t x, u
 // The drafted nodes of a sequence, held by one warp: lane l has nodes l and l + 32. seen: the
 // node itself and its ancestors as bits, reduced to those that the window and the sinks let
 // it see. A parent outside [-1, t) reads as -1 (and is reported by the status word).
+static_assert(kTreeMaxNodes == 64, "two nodes per lane, and their sets in 64 bits");
 struct Nodes {
   uint64_t seen[2];
   int depth[2];

@@ -56,7 +56,5 @@ RA_HD WinCut win_cut(const WinGeom& g, int64_t a, int64_t k0, int N) {
   c.sk = win_clip(g.sinks - k0, N);
   return c;
 }
-RA_HD bool win_whole(const WinCut& c, int N) { return c.hi == N && (c.lo == 0 || c.sk == N || c.sk >= c.lo); }
-RA_HD bool win_none(const WinCut& c) { return c.hi == 0 || (c.lo >= c.hi && c.sk == 0); }
 
 }  // namespace ringattn
