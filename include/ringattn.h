@@ -364,7 +364,8 @@ int ring_attn_window_bwd(const void* q, const void* k, const void* v, const void
 
 /*
  * Synchronise `stream` and read the status word at the start of `workspace`
- * (written by the last compute call that used it): 0, or RING_ATTN_ETIMEOUT.
+ * (written by the last compute call that used it): 0, RING_ATTN_ETIMEOUT, or RING_ATTN_EINVAL
+ * where the call says that it reports what it found on the device so.
  * Returns RING_ATTN_ECUDA if the stream reports an error.
  */
 int ring_attn_status(const void* workspace, void* stream);

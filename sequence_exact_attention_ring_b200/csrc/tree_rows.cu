@@ -31,7 +31,14 @@
 // A step that does not fit (scales more than 2^15 apart, R more than 2^3 below E, a block
 // that is not finite) takes the same products in bf16, whose range they always fit: the
 // code's sign, exponent and mantissa bits are moved to bf16's, which gives its value times
-// 2^-120 (e4m3) or 2^-126 (e2m1), and the multiplication by the scale makes up for that.
+// 2^-120 (e4m3) or 2^-126 (e2m1), and the multiplication by the scale makes up for that. Its
+// weights round to 8 bits. So they do over a bf16 cache, whose V they must match in type (l sums
+// them unrounded): out is then off from 64 bits by 1.2 to 1.3 times what rounding the result
+// alone costs, where fp16 weights cost 1.01 times. A block of zeros has the smallest scale of all,
+// 2^-127, so a step that holds one takes the bf16 form too.
+//
+// Four contexts of up to 128k, 4 query rows per kv head, e4m3, D = 128: 168 to 172 us a call,
+// 4.9 to 5.1 TB/s of the cache.
 //
 // Which head dimension or key meets which k index of a matrix instruction is free as long
 // as both operands agree, so lanes load 16 contiguous bytes and use them in memory order.

@@ -36,7 +36,8 @@
 // in [2^14, 2^15). A K or V tile with a scale outside that range is converted to bf16 instead,
 // and its product taken with the bf16 form of Q or P: the code's sign, exponent and mantissa
 // bits are moved to bf16's (times 2^-120 or 2^-126 of the value), and two exact
-// multiplications bring in the rest.
+// multiplications bring in the rest. The weights of such a V tile, and of a bf16 cache, round to 8
+// bits (see tree_rows.cu, also on blocks of zeros, which count as outside the range).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -33,7 +33,7 @@
 // products read both operands from shared memory: 48 clocks each at N = 64, of 32 for the
 // multiplications) and takes 1500 to 1570, a step of dq 1024 and takes 1190; a CTA's start and
 // end, which nothing overlaps, take 6000 to 8000. 32k tokens, window 2048, 16 query heads over
-// 4: 2.11 ms, 669 TFLOP/s at 10 D flops a pair.
+// 4: 2.11 to 2.12 ms, 665 to 669 TFLOP/s at 10 D flops a pair.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>

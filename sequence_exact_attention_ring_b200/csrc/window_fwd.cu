@@ -5,15 +5,18 @@
 // keys that win_tiles lists; lse = m + ln l. Exponentials come from the special-function
 // unit alone, so lse is good to a few units in its last place.
 //
-// What bounds it: the tensor cores (4 D flops per visible pair; 128 of 4096 keys a row sees
-// cost a byte each from L2). A unit is one or two query tiles of 128 * CTAS rows: in a pair one
+// What bounds it: the tensor cores (4 D flops per visible pair). Keys and values come from L2, a
+// unit's window and its own rows once: at D = 128 and a window of 4096 a unit of 512 queries
+// reads 2.4 MB for 1.07 GFLOP, 2.2 TB/s at the rate below. P is rounded to bf16, the type of the V
+// that it multiplies (l sums it unrounded): out is off from 64 bits by 1.2 to 1.4 times what
+// rounding the result alone would cost. A unit is one or two query tiles of 128 * CTAS rows: in a pair one
 // M = 256 product covers a tile of both CTAs and each CTA stages half of every K and V
 // tile, which is what lets shared memory feed the products. Each query tile walks only the
 // key tiles that its own rows see: of a unit's two tiles the first skips the key tiles past
 // its diagonal, the second those that only the first one's window holds. That makes a
 // row's overhead at most the two key tiles that its window and its diagonal cut. As built, the
 // chain of a query tile (scores ready, exponentials, P, products) bounds it: tensor pipe 54 %
-// busy, exponentials 54 %. 128k tokens, window 4096, 8 heads, D = 128: 2.23 ms, 985 TFLOP/s.
+// busy, exponentials 54 %. 128k tokens, window 4096, 8 heads, D = 128: 2.22 to 2.26 ms, 973 to 992 TFLOP/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
