@@ -398,7 +398,8 @@ def merge(o_parts: torch.Tensor, lse_parts: torch.Tensor, out_dtype=torch.float3
 def status(workspace: torch.Tensor, stream=None) -> int:
     """Synchronise and return the workspace status word: 0, binding.ETIMEOUT, or binding.EINVAL where a call
     met lengths, counts, parents or places on the device that it could not follow."""
-    return _b.ring_attn_status(workspace.data_ptr(), _stream_ptr(stream))
+    dev = workspace.device
+    return _call_on(dev, _b.ring_attn_status, workspace.data_ptr(), _stream_on(stream, dev))
 
 
 class HostRunner:
